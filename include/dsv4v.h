@@ -482,6 +482,87 @@ dsv4v_status dsv4v_image_visibility(int64_t n_seqs, int64_t seq_len, const int32
                                     void* mask, int elem_bytes, void* workspace, size_t ws_bytes,
                                     void* stream);
 
+/* ---------------------------------------------------------------- optimizer step
+ * What follows the backward calls of a training step ([PR], Validation: the pages train the
+ * tower; they print no optimizer): the norm of all gradients, and AdamW over a list of tensors.
+ * Both take a host array that describes the tensors; it is read during the call only.  Tensors
+ * may be empty (n = 0) and need only the alignment of their element type; 16-byte aligned ones
+ * (8-byte for 8-bit states) take the vector path. */
+
+/* One gradient: device array of n elements, fp32 or bf16. */
+typedef struct {
+  const void* data;
+  int64_t n;
+  dsv4v_dtype dtype;
+} dsv4v_grad;
+
+/* Bytes of device scratch that dsv4v_grad_norm needs for a list of n_tensors (host
+ * computation); 0 if n_tensors < 0. */
+size_t dsv4v_grad_norm_workspace_size(int n_tensors);
+
+/* norm_out (device fp32) = sqrt(sum of g^2 over every element of every tensor), summed in fp64 in
+ * an order that depends on the list alone (0 for an empty list; inf or NaN if a gradient is).
+ *   grads: host array of n_tensors; at most 2^40 elements in all (else DSV4V_ERR_UNSUPPORTED).
+ *   workspace: device, 256-byte aligned, dsv4v_grad_norm_workspace_size(n_tensors) bytes. */
+dsv4v_status dsv4v_grad_norm(const dsv4v_grad* grads, int n_tensors, float* norm_out, void* workspace,
+                             size_t ws_bytes, void* stream);
+
+/* One tensor of an AdamW step.  Device arrays of n elements, updated in place except `grad`:
+ *   param:   param_dtype.  master: the fp32 values behind a bf16 param, or NULL (then the step
+ *            starts from the param's own values); with a master, param receives its rounding.
+ *   state_bits 32: exp_avg, exp_avg_sq are fp32 [n], the scales NULL.
+ *   state_bits 8:  exp_avg, exp_avg_sq hold one e4m3 code per element, with one fp32 scale per
+ *            block of DSV4V_STATE_BLOCK elements (the last may be short): exp_avg = code * scale,
+ *            exp_avg_sq = (code * scale)^2, the code being that of its root.  A scale is the
+ *            smallest power of two (at least 2^-126) that brings its block to at most 448, 0 for a
+ *            block of zeros; codes round to nearest even, a root above zero at least to the
+ *            smallest code, and what is not finite becomes the NaN code.  All zeros is the
+ *            initial state.
+ *   weight_decay: of this tensor (norm scales and biases usually take 0).
+ * No two tensors of a list may overlap. */
+#define DSV4V_STATE_BLOCK 256
+typedef struct {
+  void* param;
+  const void* grad;
+  float* master;
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* exp_avg_scale;
+  float* exp_avg_sq_scale;
+  int64_t n;
+  dsv4v_dtype param_dtype;
+  dsv4v_dtype grad_dtype;
+  int state_bits;
+  double weight_decay;
+} dsv4v_adamw_tensor;
+
+typedef struct {
+  double lr;
+  double beta1;          /* in [0, 1) */
+  double beta2;          /* in [0, 1) */
+  double eps;            /* > 0 */
+  int64_t step;          /* number of this step, from 1 on; unused with a step_dev */
+  double max_grad_norm;  /* clip the gradients to this norm; 0: no clipping.  Needs grad_norm. */
+} dsv4v_adamw_config;
+
+/* One AdamW step (decoupled weight decay) of every tensor of the list, in fp32:
+ *   g <- grad * min(1, max_grad_norm / grad_norm)
+ *   exp_avg <- beta1 exp_avg + (1 - beta1) g;  exp_avg_sq <- beta2 exp_avg_sq + (1 - beta2) g^2
+ *   param <- param (1 - lr weight_decay)
+ *            - lr / (1 - beta1^step) * exp_avg / (sqrt(exp_avg_sq / (1 - beta2^step)) + eps)
+ * (the update takes the moments before they are rounded to 8 bits).
+ *   tensors:   host array of n_tensors; at most 2^40 elements in all.
+ *   grad_norm: device fp32 (dsv4v_grad_norm's output) or NULL.  A norm that is not finite skips
+ *              the step: nothing is written.
+ *   lr_dev:    device fp32 learning rate that replaces cfg->lr, or NULL.
+ *   step_dev:  device int64 (8-byte aligned) count of the steps taken, 0 or more, or NULL: the
+ *              call takes step *step_dev + 1 and stores that number, unless it skips the step.
+ *   With these two a captured call can be replayed while the schedule moves on.
+ * Needs no workspace.  Weights written by this call may be passed to any call that follows it on
+ * the stream. */
+dsv4v_status dsv4v_adamw_step(const dsv4v_adamw_config* cfg, const dsv4v_adamw_tensor* tensors, int n_tensors,
+                              const float* grad_norm, const float* lr_dev, int64_t* step_dev, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -48,15 +48,6 @@ bool device_info(DeviceInfo& out) {
   return true;
 }
 
-// SM count used for planning when no device can be queried (sizing only).
-int planning_sms() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) == cudaSuccess && cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
-    return sms;
-  cudaGetLastError();
-  return 148;
-}
-
 // ---------------------------------------------------------------------------- tensor maps
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -818,6 +809,27 @@ dsv4v_status prepare_rows(const dsv4v_config* cfg, int64_t rows, void* workspace
 }
 
 }  // namespace
+
+bool query_device(int* sms, uint32_t** err) {
+  DeviceInfo info;
+  if (!device_info(info)) return false;
+  if (sms) *sms = info.sms;
+  if (err) *err = info.err;
+  return true;
+}
+
+bool tensor_map_bf16(const void* ptr, int64_t rows, int64_t cols, int box_rows, int64_t ld, CUtensorMap* out) {
+  return bf16_map(ptr, rows, cols, box_rows, out, ld);
+}
+
+// SM count used for planning when no device can be queried (sizing only).
+int planning_sms() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess && cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
+    return sms;
+  cudaGetLastError();
+  return 148;
+}
 
 // Residual GEMM x <- x + a . w^T on the bf16 path with split-tile scratch supplied by the caller
 // (partials: partial_cap bytes, counters: counter_cap ints).  Used by the entry point whose

@@ -7,6 +7,15 @@
 
 namespace dsv4v {
 
+// ---------------------------------------------------------------------------- host services (api.cu)
+// SM count of the current device and its device error word (either may be NULL).
+bool query_device(int* sms, uint32_t** err);
+// SM count for sizing: the current device's, or a B200's where no device can be queried.
+int planning_sms();
+// Tensor map of a bf16 row-major [rows, cols] matrix, row stride ld elements (a multiple of 8),
+// boxes of 64 columns x box_rows rows in the 128-byte swizzle; reads outside return zeros.
+bool tensor_map_bf16(const void* ptr, int64_t rows, int64_t cols, int box_rows, int64_t ld, CUtensorMap* out);
+
 // ---------------------------------------------------------------------------- tcgen05 GEMM
 // C[M, n_out] = A[M, K] . B[n, K]^T with a fused epilogue; bf16 operands, fp32 accumulation.
 enum Epi : int {

@@ -40,9 +40,11 @@ EXPORTS = ("dsv4v_workspace_size", "dsv4v_rope2d_table", "dsv4v_block_forward", 
            "dsv4v_bridge_workspace_size", "dsv4v_merge_image_embeddings", "dsv4v_image_visibility",
            "dsv4v_backward_workspace_size", "dsv4v_attention_backward", "dsv4v_rmsnorm_backward",
            "dsv4v_block_backward", "dsv4v_tower_backward", "dsv4v_set_tower_path", "dsv4v_tower_path",
-           "dsv4v_step_launches", "dsv4v_set_graph_replay", "dsv4v_release_graphs")
+           "dsv4v_step_launches", "dsv4v_set_graph_replay", "dsv4v_release_graphs",
+           "dsv4v_grad_norm_workspace_size", "dsv4v_grad_norm", "dsv4v_adamw_step")
 
 DSV4V_NOALLOC_MAX_ROWS = 65536
+DSV4V_STATE_BLOCK = 256  # elements that share one scale of an 8-bit optimizer state
 
 
 class Dsv4vError(RuntimeError):
@@ -72,6 +74,22 @@ class BlockGrads(ctypes.Structure):
 class Batch(ctypes.Structure):
     _fields_ = [("n_images", ctypes.c_int), ("grid_hw_host", ctypes.c_void_p), ("grid_hw_dev", ctypes.c_void_p),
                 ("cu_patches_host", ctypes.c_void_p), ("cu_patches_dev", ctypes.c_void_p)]
+
+
+class Grad(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("n", ctypes.c_int64), ("dtype", ctypes.c_int)]
+
+
+class AdamwTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("master", ctypes.c_void_p),
+                ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p), ("exp_avg_scale", ctypes.c_void_p),
+                ("exp_avg_sq_scale", ctypes.c_void_p), ("n", ctypes.c_int64), ("param_dtype", ctypes.c_int),
+                ("grad_dtype", ctypes.c_int), ("state_bits", ctypes.c_int), ("weight_decay", ctypes.c_double)]
+
+
+class AdamwConfig(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", ctypes.c_int64), ("max_grad_norm", ctypes.c_double)]
 
 
 _lib = None
@@ -120,6 +138,9 @@ def lib() -> ctypes.CDLL:
             "dsv4v_step_launches": (I, [cfg, bat, I, I]),
             "dsv4v_set_graph_replay": (None, [I]),
             "dsv4v_release_graphs": (None, []),
+            "dsv4v_grad_norm_workspace_size": (SZ, [I]),
+            "dsv4v_grad_norm": (I, [P, I, P, P, SZ, P]),
+            "dsv4v_adamw_step": (I, [ctypes.POINTER(AdamwConfig), P, I, P, P, P, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -393,6 +414,121 @@ def dsv4v_tower_backward(cfg, batch, layers, final_norm_w, layer_inputs, x_last,
                                       _ptr(x_last), _ptr(d_out), _ptr(dx), grads, _ptr(d_final_norm_w),
                                       *_ws(workspace), _stream(stream)),
            "dsv4v_tower_backward")
+
+
+# ------------------------------------------------------------------------------ optimizer step
+def _dtype_code(t, what):
+    import torch
+    code = {torch.float32: DSV4V_F32, torch.bfloat16: DSV4V_BF16}.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{what} is {t.dtype}: fp32 or bf16 is wanted")
+    return code
+
+
+def _on_device(t, what, device, dtypes=None, numel=None):
+    """Checks a tensor that a table or call is about to pass as a raw pointer."""
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{what} is on {t.device}, not on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} is not contiguous")
+    if dtypes is not None and t.dtype not in dtypes:
+        raise ValueError(f"{what} is {t.dtype}: {' or '.join(str(d) for d in dtypes)} is wanted")
+    if numel is not None and t.numel() != numel:
+        raise ValueError(f"{what} has {t.numel()} elements, not {numel}")
+    return t.data_ptr()
+
+
+def _current(device, where):
+    import torch
+    if device is not None and device.index != torch.cuda.current_device():
+        raise ValueError(f"{where}: the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+class GradTable:
+    """The gradients of one dsv4v_grad_norm call (contiguous fp32 or bf16 tensors of one device),
+    kept alive here."""
+
+    def __init__(self, grads):
+        self.tensors = list(grads)
+        self.device = self.tensors[0].device if self.tensors else None
+        self.n = len(self.tensors)
+        self.c = (Grad * max(1, self.n))()
+        for i, g in enumerate(self.tensors):
+            self.c[i] = Grad(_on_device(g, f"grads[{i}]", self.device), g.numel(), _dtype_code(g, f"grads[{i}]"))
+
+
+def dsv4v_grad_norm_workspace_size(table) -> int:
+    """table: a GradTable, or the number of its tensors."""
+    return int(lib().dsv4v_grad_norm_workspace_size(table if isinstance(table, int) else table.n))
+
+
+def dsv4v_grad_norm(table: GradTable, norm_out, workspace, stream=None):
+    """norm_out (one fp32 value on the device) <- the norm over every gradient of the table."""
+    import torch
+    _current(table.device, "dsv4v_grad_norm")
+    out = _on_device(norm_out, "norm_out", table.device or norm_out.device, (torch.float32,), 1)
+    _check(lib().dsv4v_grad_norm(table.c, table.n, out, *_ws(workspace), _stream(stream)), "dsv4v_grad_norm")
+
+
+def make_adamw(lr, beta1=0.9, beta2=0.999, eps=1e-8, step=1, max_grad_norm=0.0) -> AdamwConfig:
+    """step: the number of the step taken, from 1 on (ignored by calls with a device step count)."""
+    return AdamwConfig(lr, beta1, beta2, eps, step, max_grad_norm)
+
+
+class AdamwTable:
+    """The tensors of one dsv4v_adamw_step call, kept alive here.  tensors: dicts of device
+    tensors param, grad, exp_avg, exp_avg_sq, optionally master (fp32, of a bf16 param) and
+    weight_decay (a number, 0 by default); for 8-bit states (uint8 or float8_e4m3fn exp_avg and
+    exp_avg_sq) exp_avg_scale and exp_avg_sq_scale too, fp32, one value per DSV4V_STATE_BLOCK
+    elements."""
+
+    def __init__(self, tensors):
+        import torch
+        self.tensors = [dict(t) for t in tensors]
+        self.n = len(self.tensors)
+        self.device = self.tensors[0]["param"].device if self.n else None
+        self.c = (AdamwTensor * max(1, self.n))()
+        f32, codes, written = (torch.float32,), (torch.uint8, torch.float8_e4m3fn), []
+        for i, t in enumerate(self.tensors):
+            p, g = t["param"], t["grad"]
+            n = p.numel()
+            eight = t["exp_avg"].dtype in codes
+            blocks = (n + DSV4V_STATE_BLOCK - 1) // DSV4V_STATE_BLOCK
+            want = {"param": (None, n), "grad": (None, n), "master": (f32, n),
+                    "exp_avg": (codes if eight else f32, n), "exp_avg_sq": (codes if eight else f32, n),
+                    "exp_avg_scale": (f32, blocks), "exp_avg_sq_scale": (f32, blocks)}
+            ptr = dict.fromkeys(want)
+            for key, (dtypes, numel) in want.items():
+                x = t.get(key)
+                if x is None:
+                    if key == "master" or (key.endswith("scale") and not eight):
+                        continue
+                    raise ValueError(f"tensors[{i}] has no {key}")
+                if key.endswith("scale") and not eight:
+                    raise ValueError(f"tensors[{i}] has {key}, but fp32 states")
+                ptr[key] = _on_device(x, f"tensors[{i}] {key}", self.device, dtypes, numel)
+                if key != "grad" and x.numel():
+                    written.append((x.data_ptr(), x.data_ptr() + x.numel() * x.element_size(), i))
+            self.c[i] = AdamwTensor(ptr["param"], ptr["grad"], ptr["master"], ptr["exp_avg"], ptr["exp_avg_sq"],
+                                    ptr["exp_avg_scale"], ptr["exp_avg_sq_scale"], n,
+                                    _dtype_code(p, f"tensors[{i}] param"), _dtype_code(g, f"tensors[{i}] grad"),
+                                    8 if eight else 32, float(t.get("weight_decay") or 0.0))
+        written.sort()
+        for (_, end, i), (begin, _, j) in zip(written, written[1:]):
+            if begin < end:
+                raise ValueError(f"tensors[{i}] and tensors[{j}] overlap: every tensor may be listed once")
+
+
+def dsv4v_adamw_step(cfg: AdamwConfig, table: AdamwTable, grad_norm=None, lr_dev=None, step_dev=None, stream=None):
+    """One AdamW step of every tensor of the table.  grad_norm, lr_dev: one fp32 value on the
+    device; step_dev: one int64 value on the device, advanced by the call."""
+    import torch
+    _current(table.device, "dsv4v_adamw_step")
+    args = []
+    for what, t, dtype in (("grad_norm", grad_norm, torch.float32), ("lr_dev", lr_dev, torch.float32),
+                           ("step_dev", step_dev, torch.int64)):
+        args.append(None if t is None else _on_device(t, what, table.device or t.device, (dtype,), 1))
+    _check(lib().dsv4v_adamw_step(ctypes.byref(cfg), table.c, table.n, *args, _stream(stream)), "dsv4v_adamw_step")
 
 
 def dsv4v_device_error(stream=None) -> int:
