@@ -482,6 +482,60 @@ dsv4v_status dsv4v_image_visibility(int64_t n_seqs, int64_t seq_len, const int32
                                     void* mask, int elem_bytes, void* workspace, size_t ws_bytes,
                                     void* stream);
 
+/* ---------------------------------------------------------------- Linear layer
+ * A Linear layer of any width with its gradient: what the projectors above are made of
+ * ([vision-API, DeepseekV4VisionPatchEmbed] and the PatchMerger's two Linears), for programs that
+ * build or train their own. */
+typedef enum {
+  DSV4V_ACT_NONE = 0,
+  DSV4V_ACT_GELU = 1,  /* v (1 + erf(v / sqrt 2)) / 2 */
+  DSV4V_ACT_SILU = 2   /* v / (1 + exp(-v)) */
+} dsv4v_activation;
+
+/* rows >= 0 (at most 2^30), widths from 1 to 2^21.  ld_*: row strides in elements, 0 = packed; in
+ * DSV4V_BF16, ld_x and ld_w (0 = in_features) are multiples of 8, else DSV4V_ERR_UNSUPPORTED.
+ * dtype is that of x, w, residual, z, y and of their gradients; bias and its gradient are fp32. */
+typedef struct {
+  int64_t rows;
+  int in_features;
+  int out_features;
+  int activation;       /* dsv4v_activation */
+  dsv4v_dtype dtype;
+  int64_t ld_x;         /* of x and dx */
+  int64_t ld_w;         /* of w and dw */
+  int64_t ld_residual;
+  int64_t ld_z;
+  int64_t ld_y;         /* of y and d_y */
+} dsv4v_linear;
+
+/* z = x . w^T + bias;  y = act(z) + residual.  Products accumulate in fp32 and everything after them
+ * runs in fp32; y and z are each rounded once (y from the unrounded z).
+ *   x: device [rows, in_features]; w: device [out_features, in_features]; both 16-byte aligned in
+ *   DSV4V_BF16.  bias: device fp32 [out_features], 16-byte aligned, or NULL (none).
+ *   residual: device [rows, out_features], or NULL (none); it may be y itself (then with equal row
+ *   strides), and no other two matrices may overlap.
+ *   z: device [rows, out_features], written for dsv4v_linear_backward, or NULL.
+ *   y: device [rows, out_features], written.  Elements between a row's end and the next row are
+ *   left as they were.
+ * Needs no workspace; the result does not depend on the schedule. */
+dsv4v_status dsv4v_linear_forward(const dsv4v_linear* layer, const void* x, const void* w, const float* bias,
+                                  const void* residual, void* z, void* y, void* stream);
+
+/* Bytes of device scratch that dsv4v_linear_backward needs (host computation); 0 if the layer is
+ * invalid. */
+size_t dsv4v_linear_backward_workspace_size(const dsv4v_linear* layer);
+
+/* Gradients of dsv4v_linear_forward for the output gradient d_y [rows, out_features]:
+ *   dz = d_y * act'(z) (rounded to the dtype as an operand of the two products);
+ *   dx = dz . w [rows, in_features];  dw = dz^T . x [out_features, in_features];
+ *   db = the sum over rows of the unrounded dz, fp32 [out_features].
+ * Each of dx, dw and db may be NULL (not computed) and is written, not added to.  w is read for
+ * dx, x for dw and z for an activation; the others may be NULL then.  The residual's gradient is
+ * d_y.  With rows = 0, dw and db are zeros.  No written matrix may overlap another argument. */
+dsv4v_status dsv4v_linear_backward(const dsv4v_linear* layer, const void* x, const void* w, const void* z,
+                                   const void* d_y, void* dx, void* dw, float* db, void* workspace,
+                                   size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------------- optimizer step
  * What follows the backward calls of a training step ([PR], Validation: the pages train the
  * tower; they print no optimizer): the norm of all gradients, and AdamW over a list of tensors.

@@ -1,0 +1,467 @@
+// Entry points of the Linear layer (forward and backward), the kernels around its GEMMs (the
+// gradient of the activation with the bias gradient's sums) and its fp32 CUDA-core path.
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+#include "linear.h"
+
+// No pointer here is __restrict__: the kernels start before their predecessor ends, and a load that
+// the compiler may take for invariant could move ahead of the wait for it.
+namespace dsv4v {
+
+namespace {
+
+// ---------------------------------------------------------------------------- activation gradient
+// dz = dy act'(z).  The bf16 path takes its exponentials and reciprocals from the MUFU pipe (a few
+// 2^-23, against the 2^-9 of the bf16 result); the fp32 path calls erff and expf.
+__device__ __forceinline__ float derivative(float z, int act, bool exact) {
+  if (act == DSV4V_ACT_GELU) {
+    // Phi(z) + z phi(z)
+    if (exact)
+      return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) + z * expf(-0.5f * z * z) * 0.39894228040143268f;
+    // erfc by Abramowitz and Stegun 7.1.26, |error| <= 1.5e-7; its e^(-z^2 / 2) serves phi too
+    const float t = rcp_approx(fmaf(0.3275911f * 0.70710678118654752f, fabsf(z), 1.0f));
+    float q = fmaf(1.061405429f, t, -1.453152027f);
+    q = fmaf(q, t, 1.421413741f);
+    q = fmaf(q, t, -0.284496736f);
+    q = fmaf(q, t, 0.254829592f);
+    const float ex = ex2_approx(z * z * -0.72134752044448170f);
+    const float tail = 0.5f * q * t * ex;
+    return fmaf(z * 0.39894228040143268f, ex, z >= 0.0f ? 1.0f - tail : tail);
+  }
+  if (act == DSV4V_ACT_SILU) {
+    // s (1 + z (1 - s)), s the logistic of z; far below zero s vanishes before z (1 - s) grows
+    const float s = exact ? 1.0f / (1.0f + expf(-z)) : rcp_approx(1.0f + ex2_approx(z * -1.4426950408889634f));
+    return s * fmaf(z, 1.0f - s, 1.0f);
+  }
+  return 1.0f;
+}
+
+__device__ __forceinline__ void get8(const __nv_bfloat16* p, bool whole, int cnt, float (&v)[8]) {
+  if (whole) {
+    const uint4 q = *reinterpret_cast<const uint4*>(p);
+    v[0] = bf16_lo(q.x), v[1] = bf16_hi(q.x), v[2] = bf16_lo(q.y), v[3] = bf16_hi(q.y);
+    v[4] = bf16_lo(q.z), v[5] = bf16_hi(q.z), v[6] = bf16_lo(q.w), v[7] = bf16_hi(q.w);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < cnt ? __bfloat162float(p[j]) : 0.0f;
+  }
+}
+__device__ __forceinline__ void get8(const float* p, bool whole, int cnt, float (&v)[8]) {
+  if (whole) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < cnt ? p[j] : 0.0f;
+  }
+}
+// dz lies in the workspace, its rows padded to 8 elements: whole pieces always fit.
+__device__ __forceinline__ void put8(__nv_bfloat16* p, const float (&v)[8]) {
+  *reinterpret_cast<uint4*>(p) =
+      make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+__device__ __forceinline__ void put8(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+constexpr int kDzCols = 256;  // columns of a CTA: 32 threads of 8, by 8 rows at a time
+
+// One pass over dy (and z): writes dz where it is wanted and, per strip of rows, the column sums of
+// the unrounded dz, whose strips k_column_sums adds in order.  HBM bounds it.
+template <class T>
+__global__ void __launch_bounds__(256) k_linear_dz(const T* dy, int64_t ld_dy, const T* z, int64_t ld_z,
+                                                   int act, T* dz, int64_t ld_dz, float* sums,
+                                                   int64_t rows, int n, int64_t strip, bool vec) {
+  launch_dependents();
+  grid_dependency_wait();
+  constexpr bool exact = sizeof(T) == 4;
+  __shared__ float s[8][kDzCols + 8];
+  const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
+  const int col = blockIdx.x * kDzCols + cx * 8;
+  const int cnt = min(8, n - col);
+  const bool whole = vec && cnt == 8;
+  float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (cnt > 0) {
+    const int64_t r1 = min(rows, static_cast<int64_t>(blockIdx.y + 1) * strip);
+#pragma unroll 2
+    for (int64_t r = static_cast<int64_t>(blockIdx.y) * strip + ry; r < r1; r += 8) {
+      float g[8];
+      get8(dy + r * ld_dy + col, whole, cnt, g);
+      if (act != DSV4V_ACT_NONE) {
+        float v[8];
+        get8(z + r * ld_z + col, whole, cnt, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] *= derivative(v[j], act, exact);
+      }
+      if (dz) put8(dz + r * ld_dz + col, g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] += g[j];
+    }
+  }
+  if (!sums) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s[ry][cx * 8 + j] = acc[j];
+  __syncthreads();
+  const int c = blockIdx.x * kDzCols + threadIdx.x;
+  if (c >= n) return;
+  float t = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t += s[i][threadIdx.x];
+  sums[static_cast<int64_t>(blockIdx.y) * n + c] = t;
+}
+
+__global__ void __launch_bounds__(256) k_column_sums(const float* sums, int strips, int n, float* out) {
+  launch_dependents();
+  grid_dependency_wait();
+  __shared__ float s[8][33];
+  const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + cx;
+  float t = 0.0f;
+  if (c < n)
+#pragma unroll 4
+    for (int i = ry; i < strips; i += 8) t += sums[static_cast<int64_t>(i) * n + c];
+  s[ry][cx] = t;
+  __syncthreads();
+  if (ry != 0 || c >= n) return;
+  t = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t += s[i][cx];
+  out[c] = t;
+}
+
+// ---------------------------------------------------------------------------- fp32 GEMM
+// D[M, N] = A . B^T on CUDA cores (tcgen05 has no exact fp32): 64 x 64 tiles, 16 deep, 4 x 4 outputs a
+// thread.  A_K / B_K: the contraction is the operand's contiguous index; else its M or N index is.
+// Products are summed over 128 of K at a time and these sums added up, which keeps the error near
+// that of sums of 128 + K / 128 terms.
+constexpr int FT = 64, FK = 16, kFlush = 128 / FK;
+
+template <bool K_FAST>
+__device__ __forceinline__ void load_tile(const float* a, int64_t ld, int64_t i0, int64_t n_i, int64_t k0, int64_t n_k,
+                                          float (&q)[4]) {
+  const int t = threadIdx.x;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int64_t i = i0 + (K_FAST ? t / 16 + 16 * j : t % 64), k = k0 + (K_FAST ? t % 16 : t / 64 + 4 * j);
+    q[j] = i < n_i && k < n_k ? a[K_FAST ? i * ld + k : k * ld + i] : 0.0f;
+  }
+}
+template <bool K_FAST>
+__device__ __forceinline__ void stage_tile(float (*s)[FT + 4], const float (&q)[4]) {
+  const int t = threadIdx.x;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (K_FAST) s[t % 16][t / 16 + 16 * j] = q[j];
+    else s[t / 64 + 4 * j][t % 64] = q[j];
+  }
+}
+
+struct EpilogueF32 {
+  float* y;
+  int64_t ld_y;
+  const float* bias;
+  const float* residual;
+  int64_t ld_residual;
+  float* z;
+  int64_t ld_z;
+  int act;
+};
+
+template <bool A_K, bool B_K>
+__global__ void __launch_bounds__(256) k_linear_f32(const float* a, int64_t lda, const float* b,
+                                                    int64_t ldb, int64_t M, int64_t N, int64_t K, const EpilogueF32 e) {
+  launch_dependents();
+  grid_dependency_wait();
+  __shared__ float sa[2][FK][FT + 4], sb[2][FK][FT + 4];
+  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * FT, n0 = static_cast<int64_t>(blockIdx.y) * FT;
+  float sum[4][4] = {}, part[4][4] = {};
+  float qa[4], qb[4];
+  load_tile<A_K>(a, lda, m0, M, 0, K, qa);
+  load_tile<B_K>(b, ldb, n0, N, 0, K, qb);
+  const int64_t steps = (K + FK - 1) / FK;
+  for (int64_t s = 0; s < steps; ++s) {
+    const int buf = static_cast<int>(s & 1);
+    stage_tile<A_K>(sa[buf], qa);
+    stage_tile<B_K>(sb[buf], qb);
+    __syncthreads();  // one barrier a step: the other buffer's readers passed the last one
+    if (s + 1 < steps) {
+      load_tile<A_K>(a, lda, m0, M, (s + 1) * FK, K, qa);
+      load_tile<B_K>(b, ldb, n0, N, (s + 1) * FK, K, qb);
+    }
+#pragma unroll
+    for (int k = 0; k < FK; ++k) {
+      const float4 av = *reinterpret_cast<const float4*>(&sa[buf][k][ty * 4]);
+      const float4 bv = *reinterpret_cast<const float4*>(&sb[buf][k][tx * 4]);
+      const float am[4] = {av.x, av.y, av.z, av.w}, bn[4] = {bv.x, bv.y, bv.z, bv.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) part[i][j] = fmaf(am[i], bn[j], part[i][j]);
+    }
+    if (s % kFlush == kFlush - 1 || s + 1 == steps) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          sum[i][j] += part[i][j];
+          part[i][j] = 0.0f;
+        }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t r = m0 + ty * 4 + i;
+    if (r >= M) break;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t c = n0 + tx * 4 + j;
+      if (c >= N) break;
+      float v = sum[i][j];
+      if (e.bias) v += e.bias[c];
+      if (e.z) e.z[r * e.ld_z + c] = v;
+      if (e.act == DSV4V_ACT_GELU) v = 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+      else if (e.act == DSV4V_ACT_SILU) v = v / (1.0f + expf(-v));
+      if (e.residual) v += e.residual[r * e.ld_residual + c];
+      e.y[r * e.ld_y + c] = v;
+    }
+  }
+}
+
+template <bool A_K, bool B_K>
+cudaError_t launch_f32(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t M, int64_t N, int64_t K, const EpilogueF32& e,
+                       cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>((M + FT - 1) / FT), static_cast<unsigned>((N + FT - 1) / FT));
+  return launch_pdl(k_linear_f32<A_K, B_K>, grid, dim3(256), 0, s, static_cast<const float*>(a), lda, static_cast<const float*>(b),
+                    ldb, M, N, K, e);
+}
+
+// ---------------------------------------------------------------------------- host side
+bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+constexpr int64_t kMaxRows = int64_t(1) << 30;
+constexpr int kMaxWidth = 1 << 21;  // 64-column tiles along a grid's y dimension, and tensor-map strides, stay in range
+
+struct Layer {
+  int64_t rows, k, n, ld_x, ld_w, ld_residual, ld_z, ld_y;
+  int act;
+  bool bf16;
+  size_t es;
+};
+
+dsv4v_status check_layer(const dsv4v_linear* l, Layer& o) {
+  if (!l || l->rows < 0 || l->rows > kMaxRows || l->in_features < 1 || l->out_features < 1) return DSV4V_ERR_INVALID_ARG;
+  if (l->activation != DSV4V_ACT_NONE && l->activation != DSV4V_ACT_GELU && l->activation != DSV4V_ACT_SILU)
+    return DSV4V_ERR_INVALID_ARG;
+  if (l->dtype != DSV4V_F32 && l->dtype != DSV4V_BF16) return DSV4V_ERR_INVALID_ARG;
+  if (l->in_features > kMaxWidth || l->out_features > kMaxWidth) return DSV4V_ERR_UNSUPPORTED;
+  o.rows = l->rows;
+  o.k = l->in_features;
+  o.n = l->out_features;
+  o.act = l->activation;
+  o.bf16 = l->dtype == DSV4V_BF16;
+  o.es = o.bf16 ? 2 : 4;
+  const int64_t given[5] = {l->ld_x, l->ld_w, l->ld_residual, l->ld_z, l->ld_y}, least[5] = {o.k, o.k, o.n, o.n, o.n};
+  int64_t* lds[5] = {&o.ld_x, &o.ld_w, &o.ld_residual, &o.ld_z, &o.ld_y};
+  for (int i = 0; i < 5; ++i) {
+    *lds[i] = given[i] == 0 ? least[i] : given[i];
+    if (*lds[i] < least[i]) return DSV4V_ERR_INVALID_ARG;
+    if (*lds[i] > (int64_t(1) << 32)) return DSV4V_ERR_UNSUPPORTED;
+  }
+  // TMA takes the rows of x, W (and of dx, dW's operands) in 16-byte steps.
+  if (o.bf16 && (o.ld_x % 8 || o.ld_w % 8)) return DSV4V_ERR_UNSUPPORTED;
+  return DSV4V_OK;
+}
+
+int64_t dz_ld(const Layer& l) { return (l.n + 7) / 8 * 8; }
+
+// Strips of rows of the dz pass: about four CTAs an SM, at least 32 rows each.
+int dz_strips(const Layer& l, int sms) {
+  const int64_t across = (l.n + kDzCols - 1) / kDzCols;
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((l.rows + 31) / 32, 4ll * sms / across)));
+}
+
+struct BackwardLayout {
+  size_t dz, sums, total;
+};
+BackwardLayout backward_layout(const Layer& l, int sms) {
+  BackwardLayout b{};
+  b.sums = up256(static_cast<size_t>(l.rows) * dz_ld(l) * l.es);
+  b.total = b.sums + up256(static_cast<size_t>(dz_strips(l, sms)) * l.n * sizeof(float));
+  return b;
+}
+
+dsv4v_status cuda_status(cudaError_t e) { return e == cudaSuccess ? DSV4V_OK : DSV4V_ERR_CUDA; }
+
+// One bf16 GEMM of the layer: D[M, N] over a contraction of K.  a is stored [M, K] or, for the
+// weight gradient, [K, M]; b is stored [N, K] in the forward, else [K, N].
+dsv4v_status gemm(LinearForm form, const void* a, int64_t lda, const void* b, int64_t ldb, int64_t M, int64_t N, int64_t K,
+                  const LinearEpilogue& e, cudaStream_t s) {
+  int sms = 0;
+  uint32_t* err = nullptr;
+  if (!query_device(&sms, &err)) return DSV4V_ERR_CUDA;
+  const bool a_mn = form == LINEAR_WEIGHT_GRAD, b_mn = form != LINEAR_FORWARD;
+  const LinearPlan plan = plan_linear(M, N, K, b_mn, sms);
+  if (plan.bn == 0) return DSV4V_ERR_UNSUPPORTED;
+  CUtensorMap ta, tb;
+  if (!(a_mn ? tensor_map_bf16(a, K, M, linear_box_a(true), lda, &ta) : tensor_map_bf16(a, M, K, linear_box_a(false), lda, &ta)) ||
+      !(b_mn ? tensor_map_bf16(b, K, N, linear_box_b(plan, true), ldb, &tb)
+             : tensor_map_bf16(b, N, K, linear_box_b(plan, false), ldb, &tb)))
+    return DSV4V_ERR_CUDA;
+  return cuda_status(launch_linear(form, plan, ta, tb, static_cast<int>(M), static_cast<int>(N), e, err, s));
+}
+
+bool rows16(const void* p, int64_t ld) { return !p || (aligned_to(p, 16) && ld % 8 == 0); }
+
+dsv4v_status forward(const Layer& l, const void* x, const void* w, const float* bias, const void* residual, void* z, void* y,
+                     cudaStream_t s) {
+  if (!l.bf16) {
+    const EpilogueF32 e{static_cast<float*>(y), l.ld_y, bias, static_cast<const float*>(residual), l.ld_residual,
+                        static_cast<float*>(z), l.ld_z, l.act};
+    return cuda_status(launch_f32<true, true>(x, l.ld_x, w, l.ld_w, l.rows, l.n, l.k, e, s));
+  }
+  LinearEpilogue e{};
+  e.y = static_cast<__nv_bfloat16*>(y);
+  e.ld_y = l.ld_y;
+  e.bias = bias;
+  e.residual = static_cast<const __nv_bfloat16*>(residual);
+  e.ld_residual = l.ld_residual;
+  e.z = static_cast<__nv_bfloat16*>(z);
+  e.ld_z = l.ld_z;
+  e.act = l.act;
+  e.vec_io = rows16(y, l.ld_y) && rows16(residual, l.ld_residual) && rows16(z, l.ld_z);
+  return gemm(LINEAR_FORWARD, x, l.ld_x, w, l.ld_w, l.rows, l.n, l.k, e, s);
+}
+
+template <class T>
+cudaError_t launch_dz(const Layer& l, const void* d_y, const void* z, void* dz, float* sums, int strips, cudaStream_t s) {
+  const int64_t strip = (l.rows + strips - 1) / strips;
+  const bool act = l.act != DSV4V_ACT_NONE;
+  const bool vec = aligned_to(d_y, 16) && l.ld_y * sizeof(T) % 16 == 0 && (!act || (aligned_to(z, 16) && l.ld_z * sizeof(T) % 16 == 0));
+  return launch_pdl(k_linear_dz<T>, dim3(static_cast<unsigned>((l.n + kDzCols - 1) / kDzCols), static_cast<unsigned>(strips)),
+                    dim3(256), 0, s, static_cast<const T*>(d_y), l.ld_y, static_cast<const T*>(z), l.ld_z, l.act,
+                    static_cast<T*>(dz), dz_ld(l), sums, l.rows, static_cast<int>(l.n), strip, vec);
+}
+
+dsv4v_status backward(const Layer& l, const void* x, const void* w, const void* z, const void* d_y, void* dx, void* dw, float* db,
+                      uint8_t* ws, const BackwardLayout& bl, int sms, cudaStream_t s) {
+  if (l.rows == 0) {  // sums over no rows
+    if (dw && cudaMemset2DAsync(dw, l.ld_w * l.es, 0, l.k * l.es, l.n, s) != cudaSuccess) return DSV4V_ERR_CUDA;
+    if (db && cudaMemsetAsync(db, 0, l.n * sizeof(float), s) != cudaSuccess) return DSV4V_ERR_CUDA;
+    return DSV4V_OK;
+  }
+  // dz is d_y itself without an activation, where TMA can take its rows.
+  const bool products = dx || dw;
+  const bool own_dz = l.act != DSV4V_ACT_NONE || (l.bf16 && !rows16(d_y, l.ld_y));
+  const bool write_dz = products && own_dz;
+  if (write_dz || db) {
+    const int strips = dz_strips(l, sms);
+    float* sums = db ? reinterpret_cast<float*>(ws + bl.sums) : nullptr;
+    void* dz = write_dz ? ws + bl.dz : nullptr;
+    const cudaError_t e = l.bf16 ? launch_dz<__nv_bfloat16>(l, d_y, z, dz, sums, strips, s) : launch_dz<float>(l, d_y, z, dz, sums, strips, s);
+    if (e != cudaSuccess) return DSV4V_ERR_CUDA;
+    if (db && launch_pdl(k_column_sums, dim3(static_cast<unsigned>((l.n + 31) / 32)), dim3(256), 0, s, static_cast<const float*>(sums),
+                         strips, static_cast<int>(l.n), db) != cudaSuccess)
+      return DSV4V_ERR_CUDA;
+  }
+  const void* dz = write_dz ? static_cast<const void*>(ws + bl.dz) : d_y;
+  const int64_t ld_dz = write_dz ? dz_ld(l) : l.ld_y;
+  if (!l.bf16) {
+    EpilogueF32 e{};
+    if (dx) {
+      e.y = static_cast<float*>(dx);
+      e.ld_y = l.ld_x;
+      if (launch_f32<true, false>(dz, ld_dz, w, l.ld_w, l.rows, l.k, l.n, e, s) != cudaSuccess) return DSV4V_ERR_CUDA;
+    }
+    if (dw) {
+      e.y = static_cast<float*>(dw);
+      e.ld_y = l.ld_w;
+      if (launch_f32<false, false>(dz, ld_dz, x, l.ld_x, l.n, l.k, l.rows, e, s) != cudaSuccess) return DSV4V_ERR_CUDA;
+    }
+    return DSV4V_OK;
+  }
+  LinearEpilogue e{};
+  if (dx) {
+    e.y = static_cast<__nv_bfloat16*>(dx);
+    e.ld_y = l.ld_x;
+    e.vec_io = rows16(dx, l.ld_x);
+    const dsv4v_status st = gemm(LINEAR_INPUT_GRAD, dz, ld_dz, w, l.ld_w, l.rows, l.k, l.n, e, s);
+    if (st != DSV4V_OK) return st;
+  }
+  if (dw) {
+    e.y = static_cast<__nv_bfloat16*>(dw);
+    e.ld_y = l.ld_w;
+    e.vec_io = rows16(dw, l.ld_w);
+    return gemm(LINEAR_WEIGHT_GRAD, dz, ld_dz, x, l.ld_x, l.n, l.k, l.rows, e, s);
+  }
+  return DSV4V_OK;
+}
+
+// Runs `f`, turning an exception (the descriptor cache's allocation) into a status: none may leave
+// a C entry.
+template <class F>
+dsv4v_status guarded(F&& f) {
+  try {
+    return f();
+  } catch (...) {
+    return DSV4V_ERR_CUDA;
+  }
+}
+
+}  // namespace
+
+}  // namespace dsv4v
+
+using namespace dsv4v;
+
+extern "C" {
+
+dsv4v_status dsv4v_linear_forward(const dsv4v_linear* layer, const void* x, const void* w, const float* bias, const void* residual,
+                                  void* z, void* y, void* stream) {
+  Layer l;
+  const dsv4v_status st = check_layer(layer, l);
+  if (st != DSV4V_OK) return st;
+  if (l.rows == 0) return DSV4V_OK;
+  const size_t in = l.bf16 ? 16 : 4;
+  if (!x || !w || !y || !aligned_to(x, in) || !aligned_to(w, in) || !aligned_to(y, l.es) || (bias && !aligned_to(bias, 16)) ||
+      (residual && !aligned_to(residual, l.es)) || (z && !aligned_to(z, l.es)))
+    return DSV4V_ERR_INVALID_ARG;
+  if (y == x || z == x || z == y || (z && z == residual) || (residual == y && l.ld_residual != l.ld_y)) return DSV4V_ERR_INVALID_ARG;
+  return guarded([&] { return forward(l, x, w, bias, residual, z, y, static_cast<cudaStream_t>(stream)); });
+}
+
+size_t dsv4v_linear_backward_workspace_size(const dsv4v_linear* layer) {
+  Layer l;
+  if (check_layer(layer, l) != DSV4V_OK) return 0;
+  return std::max<size_t>(256, backward_layout(l, planning_sms()).total);
+}
+
+dsv4v_status dsv4v_linear_backward(const dsv4v_linear* layer, const void* x, const void* w, const void* z, const void* d_y, void* dx,
+                                   void* dw, float* db, void* workspace, size_t ws_bytes, void* stream) {
+  Layer l;
+  const dsv4v_status st = check_layer(layer, l);
+  if (st != DSV4V_OK) return st;
+  const size_t in = l.bf16 ? 16 : 4;
+  const bool act = l.act != DSV4V_ACT_NONE;
+  if ((dw && !aligned_to(dw, l.es)) || (db && !aligned_to(db, 4)) || (dx && !aligned_to(dx, l.es))) return DSV4V_ERR_INVALID_ARG;
+  if (l.rows > 0) {
+    if (!d_y || !aligned_to(d_y, l.es) || (act && (!z || !aligned_to(z, l.es))) || (dx && (!w || !aligned_to(w, in))) ||
+        (dw && (!x || !aligned_to(x, in))))
+      return DSV4V_ERR_INVALID_ARG;
+    if (dx && (dx == d_y || dx == w || dx == z || dx == x)) return DSV4V_ERR_INVALID_ARG;
+    if (dw && (dw == x || dw == w || dw == d_y || dw == z || dw == dx)) return DSV4V_ERR_INVALID_ARG;
+  }
+  int sms = 0;
+  if (!query_device(&sms, nullptr)) return DSV4V_ERR_CUDA;
+  const BackwardLayout bl = backward_layout(l, sms);
+  if (!workspace || !aligned_to(workspace, 256) || ws_bytes < std::max<size_t>(256, bl.total)) return DSV4V_ERR_WORKSPACE;
+  return guarded([&] {
+    return backward(l, x, w, z, d_y, dx, dw, db, static_cast<uint8_t*>(workspace), bl, sms, static_cast<cudaStream_t>(stream));
+  });
+}
+
+}  // extern "C"

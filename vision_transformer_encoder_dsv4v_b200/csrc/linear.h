@@ -1,0 +1,47 @@
+// Interface between the Linear layer's entry points (linear.cu) and its tcgen05 GEMM (linear_tc.cu).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "dsv4v.h"
+
+namespace dsv4v {
+
+// What happens to an accumulator element: v + bias[col], kept in z, activated, residual added,
+// rounded once into y.
+struct LinearEpilogue {
+  __nv_bfloat16* y;
+  int64_t ld_y;
+  const float* bias;               // 16-byte aligned, or NULL
+  const __nv_bfloat16* residual;   // or NULL; may be y itself
+  int64_t ld_residual;
+  __nv_bfloat16* z;                // or NULL
+  int64_t ld_z;
+  int act;
+  bool vec_io;                     // the rows of y, residual and z are 16-byte aligned
+};
+
+enum LinearForm {
+  LINEAR_FORWARD,      // D[rows, out] = x . W^T: both operands K-major
+  LINEAR_INPUT_GRAD,   // dx[rows, in] = dz . W: dz K-major, W MN-major
+  LINEAR_WEIGHT_GRAD,  // dW[out, in] = dz^T . x: both MN-major
+};
+
+struct LinearPlan {
+  int pair = 0, bn = 0, ks = 1;  // CTA pairs; columns of a tile; K splits (cluster size)
+  int tiles_m = 0, tiles_n = 0, kb_total = 0, grid = 0;
+};
+
+// Tile, pairing and split of D[M, N] over a contraction of K, on `sms` SMs.
+LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool b_mn, int sms);
+// Rows of the boxes of A's and B's tensor maps under a plan (64 for MN-major operands).
+inline int linear_box_a(bool a_mn) { return a_mn ? 64 : 128; }
+inline int linear_box_b(const LinearPlan& p, bool b_mn) { return b_mn ? 64 : (p.pair ? p.bn / 2 : p.bn); }
+
+cudaError_t launch_linear(LinearForm form, const LinearPlan& plan, const CUtensorMap& ta, const CUtensorMap& tb, int M, int N,
+                          const LinearEpilogue& e, uint32_t* err, cudaStream_t s);
+
+}  // namespace dsv4v

@@ -1,0 +1,642 @@
+// The Linear layer on tcgen05: y = act(x W^T + b) + r and, for its backward, dx = dz W and
+// dW = dz^T x.  One GEMM kernel D[M, N] = A . B^T serves the three; what differs is how the operands
+// lie in memory (K-major: rows of the contraction; MN-major: columns) and the epilogue.
+//
+// Against the block's GEMM (gemm_tc.cu) this one takes any extent: TMA fills what lies outside the
+// tensors with zeros, and the epilogue stores row segments through shared memory, so that rows,
+// columns and row strides need not divide into tiles, boxes or vectors.
+//
+// Bounds and tiles.  What an SM takes in limits the main loop before the tensor pipe does: TMA
+// brings about 57 bytes a clock into an SM, and a 128 x N x 64 step needs (128 + N) 128 bytes for
+// 2 N clocks of MMA: 842 against 512 clocks at N = 256.  A pair of CTAs (cta_group::2) shares one B
+// tile, which leaves 575 of 512.  So large products run on pairs; single CTAs serve small ones,
+// split along K over a cluster where there are fewer tiles than SMs.  Each split writes its fp32
+// partial to its own shared memory and finishes a share of the tile, reading the partials of the
+// others through distributed shared memory in rank order: no workspace, no atomics, one result.
+//
+// Roles (320 threads): warp 0 loads by TMA, warp 1 issues the MMAs, warps 2 to 9 finish tiles.  The
+// accumulator is double-buffered in TMEM, so a tile's epilogue runs under the next tile's MMAs.
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+#include "linear.h"
+
+namespace dsv4v {
+
+namespace {
+
+constexpr int BM = 128;
+constexpr int BK = 64;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kMaxDynSmem = 232448;        // 227 KB per CTA
+constexpr int kStagingBytes = kEpiWarps * 2048;  // per epilogue warp: 32 rows x 64 bytes
+constexpr int kGroupM = 8;                 // row tiles of a raster group
+
+template <int BN, bool PAIR>
+struct Tile {
+  static constexpr int A_BYTES = BM * BK * 2;
+  static constexpr int B_ROWS = PAIR ? BN / 2 : BN;
+  static constexpr int B_BYTES = B_ROWS * BK * 2;
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int BUDGET = kMaxDynSmem - 1024 - 256 - kStagingBytes;
+  static constexpr int STAGES = BUDGET / STAGE > 8 ? 8 : BUDGET / STAGE;
+  static constexpr int TMEM_COLS = 2 * BN <= 128 ? 128 : (2 * BN <= 256 ? 256 : 512);
+  static constexpr int OFF_STAGING = STAGES * STAGE;
+  static constexpr int OFF_BARRIERS = OFF_STAGING + kStagingBytes;
+  static constexpr int SMEM = 1024 + OFF_BARRIERS + 256;
+  // Row stride, in floats, of a split's fp32 partial in the ring: 16 bytes off a multiple of 128,
+  // so that the rows of a warp's 16-byte accesses fall on different banks.
+  static constexpr int PART_LD = BN + 4;
+  static_assert(PAIR || BM * PART_LD * 4 <= STAGES * STAGE, "a partial tile has to fit the ring");
+};
+
+struct Params {
+  int M, N;              // extents of D
+  int tiles_m, tiles_n;  // BM (PAIR: 2 BM) x BN tiles
+  int kb_total;          // 64-deep steps of the contraction
+  LinearEpilogue e;
+  uint32_t* err;
+};
+
+// Tile t in an order that keeps the tiles in flight together compact (kGroupM row tiles by as many
+// column tiles as it takes), so that they share their operands in L2: with whole columns of 64 row
+// tiles a wave of the 16384 x 4096 x 4608 product would fetch 155 MB, with groups 40 MB.
+__device__ __forceinline__ void tile_at(const Params& p, int t, int& m, int& n) {
+  const int per = kGroupM * p.tiles_n, g = t / per, r = t - g * per;
+  const int rows = min(kGroupM, p.tiles_m - g * kGroupM);
+  n = r / rows;
+  m = g * kGroupM + (r - n * rows);
+}
+
+// ---------------------------------------------------------------------------- epilogue math
+// Both activations take 2^x and 1/x from the MUFU pipe (a few 2^-23 relative): two such operations
+// an element keep a tile's epilogue under its main loop, which erff and expf would not (about 30
+// instructions an element: 10,000 clocks a 128 x 256 tile).
+//
+// erf by Abramowitz and Stegun 7.1.26, |error| <= 1.5e-7: erfc(x) = poly(t) e^(-x^2), x >= 0.
+__device__ __forceinline__ float gelu_fast(float z) {
+  const float x = fabsf(z) * 0.70710678118654752f;
+  const float t = rcp_approx(fmaf(0.3275911f, x, 1.0f));
+  float q = fmaf(1.061405429f, t, -1.453152027f);
+  q = fmaf(q, t, 1.421413741f);
+  q = fmaf(q, t, -0.284496736f);
+  q = fmaf(q, t, 0.254829592f);
+  const float tail = 0.5f * q * t * ex2_approx(x * x * -1.4426950408889634f);  // (1 - erf) / 2 at |x|
+  return z * (z >= 0.0f ? 1.0f - tail : tail);
+}
+__device__ __forceinline__ float silu_fast(float z) {
+  return z * rcp_approx(1.0f + ex2_approx(z * -1.4426950408889634f));
+}
+__device__ __forceinline__ float activate(float z, int act) {
+  return act == DSV4V_ACT_GELU ? gelu_fast(z) : (act == DSV4V_ACT_SILU ? silu_fast(z) : z);
+}
+
+// 16-byte chunk `c` (0..3) of row `r` of a staging box: 32 rows of 64 bytes.  Eight lanes that
+// take one chunk of eight rows, or the chunks of two rows, meet eight different 16-byte banks.
+__device__ __forceinline__ uint4* box_at(uint8_t* box, int r, int c) {
+  return reinterpret_cast<uint4*>(box + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+}
+
+// Rows [row0, row0 + 32) x columns [col0, col0 + 32) of a bf16 matrix, between global memory and
+// a staging box: lane l takes chunk l % 4 of rows l / 4 + 8 i.  `vec`: rows are 16-byte aligned.
+__device__ __forceinline__ void fetch_box(const __nv_bfloat16* src, int64_t ld, int row0, int col0, int M, int N, bool vec,
+                                          int lane, uint4 (&q)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = row0 + (lane >> 2) + 8 * i, c = col0 + (lane & 3) * 8;
+    q[i] = make_uint4(0, 0, 0, 0);
+    if (r >= M || c >= N) continue;
+    const __nv_bfloat16* p = src + static_cast<int64_t>(r) * ld + c;
+    if (vec && c + 8 <= N) {
+      q[i] = *reinterpret_cast<const uint4*>(p);
+    } else {
+      const uint16_t* u = reinterpret_cast<const uint16_t*>(p);
+      uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c + j < N) w[j >> 1] |= static_cast<uint32_t>(u[j]) << (16 * (j & 1));
+      q[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
+// Rows that are not 16-byte aligned leave through 2-byte stores, a row's 32 columns by the 32
+// lanes, so that a store still covers whole sectors.
+__device__ __forceinline__ void store_box(__nv_bfloat16* dst, int64_t ld, int row0, int col0, int M, int N, bool vec, int lane,
+                                          uint8_t* box) {
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int lr = (lane >> 2) + 8 * i, r = row0 + lr, c = col0 + (lane & 3) * 8;
+      if (r >= M || c >= N) continue;
+      const uint4 q = *box_at(box, lr, lane & 3);
+      __nv_bfloat16* p = dst + static_cast<int64_t>(r) * ld + c;
+      if (c + 8 <= N) {
+        *reinterpret_cast<uint4*>(p) = q;
+      } else {
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        uint16_t* u = reinterpret_cast<uint16_t*>(p);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c + j < N) u[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
+      }
+    }
+  } else if (col0 + lane < N) {
+    const int rows = min(32, M - row0);
+    for (int lr = 0; lr < rows; ++lr) {
+      const uint16_t* u = reinterpret_cast<const uint16_t*>(box_at(box, lr, lane >> 3)) + (lane & 7);
+      reinterpret_cast<uint16_t*>(dst + static_cast<int64_t>(row0 + lr) * ld + col0)[lane] = *u;
+    }
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float* v) {
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+
+// ---------------------------------------------------------------------------- kernel
+// A_MN / B_MN: the operand is MN-major, loaded as 64 x 64 boxes of its stored [K, MN] matrix (atom
+// columns of 8 KB); else K-major, one box of 64 columns.  FWD: bias, activation, residual and the
+// saved pre-activation; without it D is stored as it is.  KS (cluster split-K) is the cluster's
+// size, 1 to 8.
+template <int BN, bool PAIR, bool A_MN, bool B_MN, bool FWD>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_linear(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+             const __grid_constant__ Params p, const int ks) {
+  using T = Tile<BN, PAIR>;
+  constexpr int STAGES = T::STAGES;
+  constexpr int BMT = PAIR ? 2 * BM : BM;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + T::OFF_BARRIERS);
+  uint64_t* empty = full + STAGES;
+  uint64_t* tfull = empty + STAGES;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* mma_done = tempty + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(mma_done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t crank = (PAIR || ks > 1) ? cluster_ctarank() : 0u;
+  const uint32_t rank = PAIR ? crank : 0u;  // 0: the pair's leader, which issues the MMAs
+  // This CTA's share of the contraction, and the tiles it takes.
+  const int slice = ks > 1 ? static_cast<int>(crank) : 0;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(slice) * p.kb_total / ks);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(slice + 1) * p.kb_total / ks);
+  const int span = PAIR ? 2 : ks;  // CTAs that share a tile
+  const int t_first = static_cast<int>(blockIdx.x) / span, t_step = static_cast<int>(gridDim.x) / span;
+  const int tiles = p.tiles_m * p.tiles_n;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], (PAIR ? 2 : 1) * kEpiWarps);
+    }
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_a);
+    tma_prefetch_desc(&tm_b);
+  }
+  if (warp == 1) {
+    if constexpr (PAIR) {
+      tmem_alloc_pair(tmem_holder, T::TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_holder, T::TMEM_COLS);
+      tmem_relinquish();
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if constexpr (PAIR) cluster_sync();  // both CTAs' barriers exist before any remote use
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_holder;
+  if constexpr (PAIR) {
+    // The leader's MMAs write the same TMEM columns in both CTAs.
+    if (threadIdx.x == 0 &&
+        ld_shared_cluster_u32(mapa_shared(smem_u32(const_cast<uint32_t*>(tmem_holder)), rank ^ 1u)) != tmem_base) {
+      atomicCAS(p.err, 0u, static_cast<uint32_t>(kErrPairTmem));
+      *abort_flag = 1;
+    }
+  }
+  if (threadIdx.x == 0) launch_dependents();
+  // Every role waits here, so that a bounded wait below never counts a predecessor's run.
+  grid_dependency_wait();
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ loads
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, issued = 0, issued_phase = 0;
+      bool ok = true;
+      // Both CTAs of a pair complete a stage on the leader's barrier, for which the leader posts
+      // the bytes.
+      const uint32_t full_leader = PAIR ? mapa_shared(smem_u32(full), 0) : 0u;
+      const bool posts = !PAIR || rank == 0;
+      constexpr uint32_t kTx = (PAIR ? 2 : 1) * T::STAGE;
+      auto load = [&](uint8_t* dst, const CUtensorMap* map, int s, int x, int y) {
+        if constexpr (PAIR) tma_load_2d_pair(dst, map, full_leader + 8u * s, x, y);
+        else tma_load_2d(dst, map, &full[s], x, y);
+      };
+      for (int t = t_first; ok && t < tiles; t += t_step) {
+        int mt, nt;
+        tile_at(p, t, mt, nt);
+        const int m0 = mt * BMT + static_cast<int>(rank) * BM;
+        const int n0 = nt * BN + static_cast<int>(rank) * (BN / 2) * (PAIR ? 1 : 0);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.err, kErrTimeoutProducer)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sa = smem + stage * T::STAGE;
+          uint8_t* sb = sa + T::A_BYTES;
+          if (posts) mbar_arrive_expect_tx(&full[stage], kTx);
+          if constexpr (A_MN) {
+#pragma unroll
+            for (int j = 0; j < BM / 64; ++j) load(sa + j * 8192, &tm_a, stage, m0 + 64 * j, kb * BK);
+          } else {
+            load(sa, &tm_a, stage, kb * BK, m0);
+          }
+          if constexpr (B_MN) {
+#pragma unroll
+            for (int j = 0; j < T::B_ROWS / 64; ++j) load(sb + j * 8192, &tm_b, stage, n0 + 64 * j, kb * BK);
+          } else {
+            load(sb, &tm_b, stage, kb * BK, n0);
+          }
+          issued |= 1u << stage;
+          issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      // No copy is in flight when the CTA exits: the MMAs consumed every stage, unless a wait gave
+      // up; then wait for each one here.  The second CTA of a pair has no full barrier of its own
+      // and waits for the MMAs' release of the stages that it filled.
+      volatile int never = 0;
+      for (int s = 0; s < STAGES; ++s) {
+        if (!(issued & (1u << s))) continue;
+        mbar_wait(posts ? &full[s] : &empty[s], (issued_phase >> s) & 1u, &never, p.err, kErrTimeoutProducer);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMAs
+    if (lane == 0) {
+      if (PAIR && rank != 0) {
+        volatile int never = 0;  // its TMEM is written until the leader's final commit
+        mbar_wait(mma_done, 0, &never, p.err, kErrTimeoutMma);
+      } else {
+        constexpr uint32_t idesc = idesc_bf16_mn(BMT, BN, A_MN, B_MN);
+        constexpr uint64_t kStepA = A_MN ? 128 : 2, kStepB = B_MN ? 128 : 2;  // 16 of K, in 16-byte units
+        int stage = 0, acc = 0;
+        uint32_t phase = 0, acc_phase = 0;
+        bool ok = true;
+        for (int t = t_first; ok && t < tiles; t += t_step) {
+          const bool free_acc = PAIR ? mbar_wait_cluster(&tempty[acc], acc_phase ^ 1, abort_flag, p.err, kErrTimeoutMma)
+                                     : mbar_wait(&tempty[acc], acc_phase ^ 1, abort_flag, p.err, kErrTimeoutMma);
+          if (!free_acc) break;
+          tc_fence_after_sync();
+          const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+          for (int kb = kb0; kb < kb1; ++kb) {
+            if (!mbar_wait(&full[stage], phase, abort_flag, p.err, kErrTimeoutMma)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after_sync();
+            const uint32_t a_addr = smem_u32(smem + stage * T::STAGE);
+            const uint64_t adesc = sdesc_sw128(a_addr, A_MN ? 8192 : 16, 1024);
+            const uint64_t bdesc = sdesc_sw128(a_addr + T::A_BYTES, B_MN ? 8192 : 16, 1024);
+#pragma unroll
+            for (int k = 0; k < BK / 16; ++k) {
+              const uint32_t accum = (kb > kb0 || k > 0) ? 1u : 0u;
+              if constexpr (PAIR) umma_bf16_pair(d_tmem, adesc + kStepA * k, bdesc + kStepB * k, idesc, accum);
+              else umma_bf16(d_tmem, adesc + kStepA * k, bdesc + kStepB * k, idesc, accum);
+            }
+            if constexpr (PAIR) umma_commit_pair(&empty[stage]);
+            else umma_commit(&empty[stage]);
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1;
+            }
+          }
+          if (!ok) break;
+          if constexpr (PAIR) umma_commit_pair(&tfull[acc]);
+          else umma_commit(&tfull[acc]);
+          if (++acc == 2) {
+            acc = 0;
+            acc_phase ^= 1;
+          }
+        }
+        // Every MMA issued completes before TMEM is released.
+        if constexpr (PAIR) umma_commit_pair(mma_done);
+        else umma_commit(mma_done);
+        volatile int never = 0;
+        mbar_wait(mma_done, 0, &never, p.err, kErrTimeoutMma);
+      }
+    }
+    __syncwarp();
+    if (!PAIR && ks > 1) {
+      cluster_sync();
+      cluster_sync();
+    }
+  } else {
+    // ------------------------------------------------------------------ epilogue
+    const int quad = warp & 3;           // TMEM lanes [32 quad, 32 quad + 32) belong to this warp
+    const int half = (warp - 2) >> 2;    // column groups half, half + 2, ...
+    const LinearEpilogue& e = p.e;
+    constexpr int NG = BN / 32;
+    uint8_t* box = smem + T::OFF_STAGING + (warp - 2) * 2048;
+    const uint32_t tempty_leader = PAIR ? mapa_shared(smem_u32(tempty), 0) : 0u;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    if (PAIR || ks == 1) {
+      for (int t = t_first; t < tiles; t += t_step) {
+        int mt, nt;
+        tile_at(p, t, mt, nt);
+        const int row0 = mt * BMT + static_cast<int>(rank) * BM + quad * 32;
+        const int n0 = nt * BN;
+        uint4 res[4];
+        if (FWD && e.residual) fetch_box(e.residual, e.ld_residual, row0, n0 + 32 * half, p.M, p.N, e.vec_io, lane, res);
+        const bool got = mbar_wait(&tfull[acc], acc_phase, abort_flag, p.err, kErrTimeoutEpilogue);
+        if (!__all_sync(0xffffffffu, got)) break;
+        tc_fence_after_sync();
+        const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(acc * BN);
+#pragma unroll 1
+        for (int g = half; g < NG; g += 2) {
+          uint32_t r[32];
+          tmem_ld32(t_row + g * 32, r);
+          if (FWD && e.residual) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) *box_at(box, (lane >> 2) + 8 * i, lane & 3) = res[i];
+            if (g + 2 < NG) fetch_box(e.residual, e.ld_residual, row0, n0 + 32 * (g + 2), p.M, p.N, e.vec_io, lane, res);
+            __syncwarp();
+          }
+          tmem_ld_wait(r);
+          if (g + 2 >= NG) {  // this warp's last read of the accumulator
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+              if constexpr (PAIR) mbar_arrive_cluster(tempty_leader + 8u * static_cast<uint32_t>(acc));
+              else mbar_arrive(&tempty[acc]);
+            }
+          }
+          const int col0 = n0 + 32 * g;
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+          if constexpr (FWD) {
+            if (e.bias) {
+              if (col0 + 32 <= p.N) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                  const float4 b = reinterpret_cast<const float4*>(e.bias + col0)[q];
+                  v[4 * q] += b.x, v[4 * q + 1] += b.y, v[4 * q + 2] += b.z, v[4 * q + 3] += b.w;
+                }
+              } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (col0 + j < p.N) v[j] += e.bias[col0 + j];
+              }
+            }
+            uint4 own_res[4];
+            if (e.residual) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) own_res[c] = *box_at(box, lane, c);
+              __syncwarp();
+            }
+            if (e.z) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) *box_at(box, lane, c) = pack8(v + 8 * c);
+              __syncwarp();
+              store_box(e.z, e.ld_z, row0, col0, p.M, p.N, e.vec_io, lane, box);
+              __syncwarp();
+            }
+            if (e.act == DSV4V_ACT_GELU) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = gelu_fast(v[j]);
+            } else if (e.act == DSV4V_ACT_SILU) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = silu_fast(v[j]);
+            }
+            if (e.residual) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const uint32_t w[4] = {own_res[c].x, own_res[c].y, own_res[c].z, own_res[c].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  v[8 * c + 2 * j] += bf16_lo(w[j]);
+                  v[8 * c + 2 * j + 1] += bf16_hi(w[j]);
+                }
+              }
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) *box_at(box, lane, c) = pack8(v + 8 * c);
+          __syncwarp();
+          store_box(e.y, e.ld_y, row0, col0, p.M, p.N, e.vec_io, lane, box);
+          __syncwarp();
+        }
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1;
+        }
+      }
+    } else {
+      // Cluster split-K: one tile a cluster.  The partial goes to the ring, which the MMAs are
+      // done with; only rows that exist are kept.
+      int mt, nt;
+      tile_at(p, t_first, mt, nt);
+      const int m0 = mt * BM, n0 = nt * BN;
+      const int rows = min(BM, p.M - m0);
+      const bool got = mbar_wait(&tfull[0], 0, abort_flag, p.err, kErrTimeoutEpilogue);
+      const bool all_got = __all_sync(0xffffffffu, got);
+      tc_fence_after_sync();
+      float* part = reinterpret_cast<float*>(smem);
+      if (all_got && quad * 32 < rows) {
+        const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+#pragma unroll 1
+        for (int g = half; g < NG; g += 2) {
+          uint32_t r[32];
+          tmem_ld32(t_row + g * 32, r);
+          tmem_ld_wait(r);
+          if (quad * 32 + lane < rows) {
+            float4* dst = reinterpret_cast<float4*>(part + (quad * 32 + lane) * T::PART_LD + g * 32);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              dst[q] = make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]), __uint_as_float(r[4 * q + 2]),
+                                   __uint_as_float(r[4 * q + 3]));
+          }
+        }
+      }
+      __syncwarp();
+      cluster_sync();
+      // The tile's 8-column pieces are dealt to the ranks in turn; a piece is summed in rank order.
+      constexpr int PIECES = BN / 8;
+      const uint32_t base = smem_u32(part);
+      for (int i = (static_cast<int>(threadIdx.x) - 64) * ks + slice; i < rows * PIECES; i += 32 * kEpiWarps * ks) {
+        const int lr = i / PIECES, c = (i - lr * PIECES) * 8;
+        const int row = m0 + lr, col = n0 + c;
+        if (col >= p.N) continue;
+        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        const uint32_t at = base + static_cast<uint32_t>(lr * T::PART_LD + c) * 4u;
+#pragma unroll 4
+        for (int k = 0; k < ks; ++k) {
+          const uint32_t remote = mapa_shared(at, static_cast<uint32_t>(k));
+          const float4 a = ld_shared_cluster_f4(remote), b = ld_shared_cluster_f4(remote + 16);
+          v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w, v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+        }
+        const int n = min(8, p.N - col);
+        const bool whole = e.vec_io && n == 8;
+        auto put = [&](__nv_bfloat16* dst) {
+          if (whole) {
+            *reinterpret_cast<uint4*>(dst) = pack8(v);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (j < n) dst[j] = __float2bfloat16_rn(v[j]);
+          }
+        };
+        if constexpr (FWD) {
+          if (e.bias) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (j < n) v[j] += e.bias[col + j];
+          }
+          if (e.z) put(e.z + static_cast<int64_t>(row) * e.ld_z + col);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = activate(v[j], e.act);
+          if (e.residual) {
+            const __nv_bfloat16* r = e.residual + static_cast<int64_t>(row) * e.ld_residual + col;
+            if (whole) {
+              const uint4 q = *reinterpret_cast<const uint4*>(r);
+              const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) v[2 * j] += bf16_lo(w[j]), v[2 * j + 1] += bf16_hi(w[j]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (j < n) v[j] += __bfloat162float(r[j]);
+            }
+          }
+        }
+        put(e.y + static_cast<int64_t>(row) * e.ld_y + col);
+      }
+      __syncwarp();
+      cluster_sync();  // no CTA leaves while another still reads its partial
+    }
+  }
+  if (!PAIR && ks > 1 && warp == 0) {
+    cluster_sync();
+    cluster_sync();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if constexpr (PAIR) cluster_sync();  // neither CTA leaves while the other may signal its barriers
+  if (warp == 1) {
+    tc_fence_after_sync();
+    if constexpr (PAIR) tmem_dealloc_pair(tmem_base, T::TMEM_COLS);
+    else tmem_dealloc(tmem_base, T::TMEM_COLS);
+  }
+}
+
+template <int BN, bool PAIR, bool A_MN, bool B_MN, bool FWD>
+cudaError_t launch_tile(const LinearPlan& plan, const CUtensorMap& ta, const CUtensorMap& tb, const Params& p, cudaStream_t s) {
+  using T = Tile<BN, PAIR>;
+  auto kern = k_linear<BN, PAIR, A_MN, B_MN, FWD>;
+  static thread_local uint64_t ready = 0;  // devices on which the shared-memory limit is raised
+  int dev = 0;
+  if (cudaError_t e = cudaGetDevice(&dev)) return e;
+  if (dev >= 64 || !(ready >> dev & 1u)) {
+    if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM)) return e;
+    if (dev < 64) ready |= uint64_t(1) << dev;
+  }
+  const unsigned span = PAIR ? 2u : static_cast<unsigned>(plan.ks);
+  if (span == 1) return launch_pdl(kern, dim3(plan.grid), dim3(kThreads), T::SMEM, s, ta, tb, p, 1);
+  return launch_pdl_cluster(kern, dim3(plan.grid), dim3(kThreads), T::SMEM, s, span, ta, tb, p, PAIR ? 1 : plan.ks);
+}
+
+template <bool A_MN, bool B_MN, bool FWD>
+cudaError_t launch_form(const LinearPlan& plan, const CUtensorMap& ta, const CUtensorMap& tb, const Params& p, cudaStream_t s) {
+  if (plan.pair) {
+    if constexpr (!B_MN) {
+      if (plan.bn == 192) return launch_tile<192, true, A_MN, B_MN, FWD>(plan, ta, tb, p, s);
+    }
+    if (plan.bn == 128) return launch_tile<128, true, A_MN, B_MN, FWD>(plan, ta, tb, p, s);
+    if (plan.bn == 256) return launch_tile<256, true, A_MN, B_MN, FWD>(plan, ta, tb, p, s);
+    return cudaErrorInvalidValue;
+  }
+  if (plan.bn == 64) return launch_tile<64, false, A_MN, B_MN, FWD>(plan, ta, tb, p, s);
+  if (plan.bn == 128) return launch_tile<128, false, A_MN, B_MN, FWD>(plan, ta, tb, p, s);
+  if (plan.bn == 256) return launch_tile<256, false, A_MN, B_MN, FWD>(plan, ta, tb, p, s);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool b_mn, int sms) {
+  // Clocks of one SM, by what bounds it (see the top): a step takes the longer of its intake at 57
+  // bytes a clock and its MMAs at 2 clocks a column; a tile's epilogue about 14 clocks a column,
+  // under the next tile's steps where there is one.
+  constexpr double kIntake = 57.0, kStart = 2500.0, kEpilogue = 14.0;
+  LinearPlan best;
+  double best_cost = 1e300;
+  const int64_t kb = (K + BK - 1) / BK;
+  for (int pair = 1; pair >= 0; --pair)
+    for (int bn : {256, 192, 128, 64}) {
+      if (pair ? (bn == 64 || (bn == 192 && b_mn)) : bn == 192) continue;
+      const int64_t bm = pair ? 2 * BM : BM;
+      const int64_t tm = (M + bm - 1) / bm, tn = (N + bn - 1) / bn, tiles = tm * tn;
+      if (tiles > (int64_t(1) << 30)) continue;
+      const double step = std::max(2.0 * bn, (BM + (pair ? bn / 2 : bn)) * 128 / kIntake);
+      for (int ks = 1; ks <= (pair ? 1 : 8); ks *= 2) {
+        if (ks > 1 && (tiles * ks > sms || kb < 2 * ks)) break;
+        const int64_t slots = pair ? sms / 2 : sms / ks;
+        if (slots < 1) break;
+        const int64_t waves = (tiles + slots - 1) / slots;
+        const double main = step * static_cast<double>((kb + ks - 1) / ks);
+        double epilogue = kEpilogue * bn;
+        if (ks > 1) epilogue = 1500.0 + epilogue / 2 + 3.0 * bn;  // to shared memory, barriers, a share of the tile
+        const double cost = kStart + main + (waves - 1) * std::max(main, epilogue) + epilogue;
+        if (cost < best_cost * (1 - 1e-9)) {
+          best_cost = cost;
+          best.pair = pair;
+          best.bn = bn;
+          best.ks = ks;
+          best.tiles_m = static_cast<int>(tm);
+          best.tiles_n = static_cast<int>(tn);
+          best.kb_total = static_cast<int>(kb);
+          best.grid = static_cast<int>(pair ? 2 * std::min<int64_t>(tiles, slots) : (ks > 1 ? tiles * ks : std::min<int64_t>(tiles, slots)));
+        }
+      }
+    }
+  return best;
+}
+
+cudaError_t launch_linear(LinearForm form, const LinearPlan& plan, const CUtensorMap& ta, const CUtensorMap& tb, int M, int N,
+                          const LinearEpilogue& e, uint32_t* err, cudaStream_t s) {
+  Params p{};
+  p.M = M;
+  p.N = N;
+  p.tiles_m = plan.tiles_m;
+  p.tiles_n = plan.tiles_n;
+  p.kb_total = plan.kb_total;
+  p.e = e;
+  p.err = err;
+  switch (form) {
+    case LINEAR_FORWARD: return launch_form<false, false, true>(plan, ta, tb, p, s);
+    case LINEAR_INPUT_GRAD: return launch_form<false, true, false>(plan, ta, tb, p, s);
+    case LINEAR_WEIGHT_GRAD: return launch_form<true, true, false>(plan, ta, tb, p, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace dsv4v

@@ -41,9 +41,11 @@ EXPORTS = ("dsv4v_workspace_size", "dsv4v_rope2d_table", "dsv4v_block_forward", 
            "dsv4v_backward_workspace_size", "dsv4v_attention_backward", "dsv4v_rmsnorm_backward",
            "dsv4v_block_backward", "dsv4v_tower_backward", "dsv4v_set_tower_path", "dsv4v_tower_path",
            "dsv4v_step_launches", "dsv4v_set_graph_replay", "dsv4v_release_graphs",
+           "dsv4v_linear_forward", "dsv4v_linear_backward_workspace_size", "dsv4v_linear_backward",
            "dsv4v_grad_norm_workspace_size", "dsv4v_grad_norm", "dsv4v_adamw_step")
 
 DSV4V_NOALLOC_MAX_ROWS = 65536
+ACT_NONE, ACT_GELU, ACT_SILU = 0, 1, 2  # DSV4V_ACT_*
 DSV4V_STATE_BLOCK = 256  # elements that share one scale of an 8-bit optimizer state
 
 
@@ -74,6 +76,12 @@ class BlockGrads(ctypes.Structure):
 class Batch(ctypes.Structure):
     _fields_ = [("n_images", ctypes.c_int), ("grid_hw_host", ctypes.c_void_p), ("grid_hw_dev", ctypes.c_void_p),
                 ("cu_patches_host", ctypes.c_void_p), ("cu_patches_dev", ctypes.c_void_p)]
+
+
+class Linear(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("in_features", ctypes.c_int), ("out_features", ctypes.c_int),
+                ("activation", ctypes.c_int), ("dtype", ctypes.c_int), ("ld_x", ctypes.c_int64), ("ld_w", ctypes.c_int64),
+                ("ld_residual", ctypes.c_int64), ("ld_z", ctypes.c_int64), ("ld_y", ctypes.c_int64)]
 
 
 class Grad(ctypes.Structure):
@@ -138,6 +146,9 @@ def lib() -> ctypes.CDLL:
             "dsv4v_step_launches": (I, [cfg, bat, I, I]),
             "dsv4v_set_graph_replay": (None, [I]),
             "dsv4v_release_graphs": (None, []),
+            "dsv4v_linear_forward": (I, [ctypes.POINTER(Linear), P, P, P, P, P, P, P]),
+            "dsv4v_linear_backward_workspace_size": (SZ, [ctypes.POINTER(Linear)]),
+            "dsv4v_linear_backward": (I, [ctypes.POINTER(Linear), P, P, P, P, P, P, P, P, SZ, P]),
             "dsv4v_grad_norm_workspace_size": (SZ, [I]),
             "dsv4v_grad_norm": (I, [P, I, P, P, SZ, P]),
             "dsv4v_adamw_step": (I, [ctypes.POINTER(AdamwConfig), P, I, P, P, P, P]),
@@ -416,6 +427,64 @@ def dsv4v_tower_backward(cfg, batch, layers, final_norm_w, layer_inputs, x_last,
            "dsv4v_tower_backward")
 
 
+# ------------------------------------------------------------------------------ Linear layer
+def make_linear(rows, in_features, out_features, activation=ACT_NONE, dtype=DSV4V_BF16, ld_x=0, ld_w=0, ld_residual=0,
+                ld_z=0, ld_y=0) -> Linear:
+    """A dsv4v_linear; row strides in elements, 0 = packed."""
+    return Linear(rows, in_features, out_features, activation, dtype, ld_x, ld_w, ld_residual, ld_z, ld_y)
+
+
+def _matrix(t, what, rows, cols, ld, layer, device):
+    """The address of a [rows, cols] matrix of the layer's dtype with row stride ld (0: cols), checked."""
+    if t is None:
+        return None
+    import torch
+    if t.dtype != (torch.bfloat16 if layer.dtype == DSV4V_BF16 else torch.float32):
+        raise ValueError(f"{what} is {t.dtype}, the layer is not")
+    if tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, not {(rows, cols)}")
+    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) != (ld or cols)):
+        raise ValueError(f"{what} has strides {t.stride()}, not {(ld or cols, 1)}")
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, not on {device}")
+    return t.data_ptr()
+
+
+def _vector(t, what, n, device):
+    import torch
+    return None if t is None else _on_device(t, what, device, (torch.float32,), n)
+
+
+def dsv4v_linear_forward(layer: Linear, x, w, bias, residual, z, y, stream=None):
+    """y = act(x . w^T + bias) + residual; z (the activation's input), bias and residual may be None."""
+    m, k, n, device = layer.rows, layer.in_features, layer.out_features, y.device
+    _current(device, "dsv4v_linear_forward")
+    _check(lib().dsv4v_linear_forward(ctypes.byref(layer), _matrix(x, "x", m, k, layer.ld_x, layer, device),
+                                      _matrix(w, "w", n, k, layer.ld_w, layer, device), _vector(bias, "bias", n, device),
+                                      _matrix(residual, "residual", m, n, layer.ld_residual, layer, device),
+                                      _matrix(z, "z", m, n, layer.ld_z, layer, device),
+                                      _matrix(y, "y", m, n, layer.ld_y, layer, device), _stream(stream)),
+           "dsv4v_linear_forward")
+
+
+def dsv4v_linear_backward_workspace_size(layer: Linear) -> int:
+    return int(lib().dsv4v_linear_backward_workspace_size(ctypes.byref(layer)))
+
+
+def dsv4v_linear_backward(layer: Linear, x, w, z, d_y, dx, dw, db, workspace, stream=None):
+    """dx, dw, db (each may be None) <- the gradients of dsv4v_linear_forward for d_y."""
+    m, k, n, device = layer.rows, layer.in_features, layer.out_features, d_y.device
+    _current(device, "dsv4v_linear_backward")
+    _check(lib().dsv4v_linear_backward(ctypes.byref(layer), _matrix(x, "x", m, k, layer.ld_x, layer, device),
+                                       _matrix(w, "w", n, k, layer.ld_w, layer, device),
+                                       _matrix(z, "z", m, n, layer.ld_z, layer, device),
+                                       _matrix(d_y, "d_y", m, n, layer.ld_y, layer, device),
+                                       _matrix(dx, "dx", m, k, layer.ld_x, layer, device),
+                                       _matrix(dw, "dw", n, k, layer.ld_w, layer, device), _vector(db, "db", n, device),
+                                       *_ws(workspace), _stream(stream)),
+           "dsv4v_linear_backward")
+
+
 # ------------------------------------------------------------------------------ optimizer step
 def _dtype_code(t, what):
     import torch
@@ -440,7 +509,11 @@ def _on_device(t, what, device, dtypes=None, numel=None):
 
 def _current(device, where):
     import torch
-    if device is not None and device.index != torch.cuda.current_device():
+    if device is None:
+        return
+    if device.type != "cuda":
+        raise ValueError(f"{where}: the tensors are on {device}")
+    if device.index != torch.cuda.current_device():
         raise ValueError(f"{where}: the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
 
 
