@@ -594,7 +594,7 @@ typedef struct {
   double lr;
   double beta1;          /* in [0, 1) */
   double beta2;          /* in [0, 1) */
-  double eps;            /* > 0 */
+  double eps;            /* a normal fp32 value above 0 */
   int64_t step;          /* number of this step, from 1 on; unused with a step_dev */
   double max_grad_norm;  /* clip the gradients to this norm; 0: no clipping.  Needs grad_norm. */
 } dsv4v_adamw_config;

@@ -4,9 +4,9 @@
 // Both read every tensor once and do a handful of operations per element, so HBM bounds them.
 // The tensor list travels in the kernel's parameters (the constant bank): no device copy of it to
 // keep, to stage or to race with, and a captured launch holds its own.  The tensors are cut into
-// chunks numbered through the list, and every CTA walks an equal, contiguous range of chunks: one
-// search for the first chunk's tensor, then steps along the list.  Lists longer than a table are
-// taken in several launches.
+// chunks numbered through the list and dealt to the CTAs in turn, so that the many small or ragged
+// tensors of a list do not gather in a few CTAs (contiguous ranges left the SMs idle for 30% of
+// the time).  Lists longer than a table are taken in several launches.
 #include <cuda_fp8.h>
 #include <algorithm>
 #include <cmath>
@@ -20,9 +20,12 @@ namespace dsv4v {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kParamBytes = 32000;  // of the 32,764 bytes that a kernel may take
+// Bytes of a table: nearly all of the 32,764 that a kernel may take or, for short lists, fewer,
+// which a launch copies sooner (65 tensors: 10.2 us a call from the host, against 11.5 us).
+constexpr int kParamBytes = 32000, kShortBytes = 8000;
 
-// Elements i .. i + 7 of a bf16 or fp32 array, as fp32; `cnt` of them exist (the rest read as 0).
+// Elements i .. i + 7 of a bf16 or fp32 array, as fp32; `cnt` of them exist (the rest read as 0;
+// with cnt <= 0, element i + cnt - 1 does).
 __device__ __forceinline__ void load8(const void* base, bool bf16, bool vec, int64_t i, int cnt, float (&v)[8]) {
   if (vec && cnt == 8) {
     if (bf16) {
@@ -36,12 +39,15 @@ __device__ __forceinline__ void load8(const void* base, bool bf16, bool vec, int
     }
     return;
   }
+  // Every load reads an element that exists, so that none waits for a branch.
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    v[j] = 0.0f;
-    if (j < cnt)
-      v[j] = bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(base)[i + j]) : static_cast<const float*>(base)[i + j];
+    const int64_t at = i + min(j, cnt - 1);
+    v[j] = bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(base)[at]) : static_cast<const float*>(base)[at];
   }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j >= cnt) v[j] = 0.0f;
 }
 
 __device__ __forceinline__ void store8(void* base, bool bf16, bool vec, int64_t i, int cnt, const float (&v)[8]) {
@@ -64,9 +70,17 @@ __device__ __forceinline__ void store8(void* base, bool bf16, bool vec, int64_t 
   }
 }
 
-// Chunks [lo, hi) of CTA `b` of `g`.
-__device__ __forceinline__ uint32_t chunk_begin(uint32_t b, uint32_t g, uint32_t chunks) {
-  return static_cast<uint32_t>(static_cast<uint64_t>(b) * chunks / g);
+// Tensor of chunk c, which lies at tensor `lo` or behind it.
+template <class Table>
+__device__ __forceinline__ int tensor_of(const Table& t, uint32_t c, int lo) {
+  if (lo + 1 >= t.count || t.e[lo + 1].chunk0 > c) return lo;
+  int hi = t.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (t.e[mid].chunk0 <= c) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
 }
 
 // ---------------------------------------------------------------------------- gradient norm
@@ -79,26 +93,34 @@ struct NormEntry {
   uint32_t chunk0;  // number of this tensor's first chunk
   uint32_t flags;   // 1: bf16, 2: 16-byte aligned
 };
-constexpr int kNormCap = (kParamBytes - 64) / static_cast<int>(sizeof(NormEntry));
+template <int BYTES>
 struct NormTable {
+  static constexpr int CAP = (BYTES - 64) / static_cast<int>(sizeof(NormEntry));
   double* partials;
   uint32_t chunks;
   int count;
-  NormEntry e[kNormCap];
+  NormEntry e[CAP];
 };
+constexpr int kNormCap = NormTable<kParamBytes>::CAP;
 
-// Sum of squares of 8 values.  fp32 (relative error of a few 2^-24, which the outer fp64 sum
+// Sum of squares of N values.  fp32 (relative error of a few 2^-24, which the outer fp64 sum
 // averages out) unless the squares leave fp32's range, which a second look in fp64 covers: the
 // norm holds for every finite gradient.
-__device__ __forceinline__ double squares8(const float (&v)[8]) {
+template <int N>
+__device__ __forceinline__ double squares(const float (&v)[N]) {
   float s = 0.0f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) s = fmaf(v[j], v[j], s);
+  for (int j = 0; j < N; ++j) s = fmaf(v[j], v[j], s);
   if (s > 1e-30f && s < 1e37f) return static_cast<double>(s);
   double d = 0.0;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) d = fma(static_cast<double>(v[j]), static_cast<double>(v[j]), d);
+  for (int j = 0; j < N; ++j) d = fma(static_cast<double>(v[j]), static_cast<double>(v[j]), d);
   return d;
+}
+
+__device__ __forceinline__ void unpack8(const uint4& q, float* v) {
+  v[0] = bf16_lo(q.x), v[1] = bf16_hi(q.x), v[2] = bf16_lo(q.y), v[3] = bf16_hi(q.y);
+  v[4] = bf16_lo(q.z), v[5] = bf16_hi(q.z), v[6] = bf16_lo(q.w), v[7] = bf16_hi(q.w);
 }
 
 // Sum over the block in a fixed order; thread 0 holds it.
@@ -115,30 +137,54 @@ __device__ __forceinline__ double block_sum(double v) {
   return s;
 }
 
-__global__ void __launch_bounds__(kThreads, 4) k_grad_norm(const __grid_constant__ NormTable t) {
+// 64 bytes of a thread are in flight at a time for bf16 and 128 for fp32, 64 to 128 KB an SM, which
+// is what hides HBM's latency.
+template <int BYTES>
+__global__ void __launch_bounds__(kThreads, 4) k_grad_norm(const __grid_constant__ NormTable<BYTES> t) {
   launch_dependents();
   grid_dependency_wait();
-  const uint32_t c0 = chunk_begin(blockIdx.x, gridDim.x, t.chunks), c1 = chunk_begin(blockIdx.x + 1, gridDim.x, t.chunks);
-  int lo = 0, hi = t.count - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (t.e[mid].chunk0 <= c0) lo = mid;
-    else hi = mid - 1;
-  }
   double acc = 0.0;
-  for (uint32_t c = c0; c < c1; ++c) {
-    while (lo + 1 < t.count && t.e[lo + 1].chunk0 <= c) ++lo;
+  int lo = 0;
+  for (uint32_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
+    lo = tensor_of(t, c, lo);
     const NormEntry& e = t.e[lo];
     const bool bf16 = e.flags & 1u, vec = e.flags & 2u;
-    const int64_t i0 = static_cast<int64_t>(c - e.chunk0) * kNormChunk + threadIdx.x * 8;
-    float v[4][8];
+    const int64_t i0 = static_cast<int64_t>(c - e.chunk0) * kNormChunk;
+    if (vec && i0 + kNormChunk <= e.n) {
+      if (bf16) {
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(e.data) + i0) + threadIdx.x;
+        uint4 q[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int64_t i = i0 + u * kThreads * 8;
-      load8(e.data, bf16, vec, i, static_cast<int>(max(int64_t(0), min(int64_t(8), e.n - i))), v[u]);
+        for (int u = 0; u < 4; ++u) q[u] = p[u * kThreads];
+#pragma unroll
+        for (int u = 0; u < 4; u += 2) {
+          float v[16];
+          unpack8(q[u], v);
+          unpack8(q[u + 1], v + 8);
+          acc += squares(v);
+        }
+      } else {
+        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(e.data) + i0) + threadIdx.x;
+        float4 q[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) q[u] = p[u * kThreads];
+#pragma unroll
+        for (int u = 0; u < 8; u += 4) {
+          const float v[16] = {q[u].x, q[u].y, q[u].z, q[u].w, q[u + 1].x, q[u + 1].y, q[u + 1].z, q[u + 1].w,
+                               q[u + 2].x, q[u + 2].y, q[u + 2].z, q[u + 2].w, q[u + 3].x, q[u + 3].y, q[u + 3].z, q[u + 3].w};
+          acc += squares(v);
+        }
+      }
+      continue;
     }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) acc += squares8(v[u]);
+#pragma unroll 1
+    for (int u = 0; u < 4; ++u) {
+      const int64_t i = i0 + (u * kThreads + threadIdx.x) * 8;
+      if (i >= e.n) break;
+      float v[8];
+      load8(e.data, bf16, vec, i, static_cast<int>(min(int64_t(8), e.n - i)), v);
+      acc += squares(v);
+    }
   }
   const double s = block_sum<kThreads>(acc);
   if (threadIdx.x == 0) t.partials[blockIdx.x] = s;
@@ -160,7 +206,7 @@ __global__ void __launch_bounds__(kThreads) k_grad_norm_final(const double* part
 constexpr int kStateBlock = 256;
 constexpr int kAdamChunk = kThreads * 8;
 
-enum : uint32_t { kParamBf16 = 1, kGradBf16 = 2, kState8 = 4, kVector = 8 };
+enum : uint32_t { kParamBf16 = 1, kGradBf16 = 2, kState8 = 4, kMaster = 8, kVector = 16 };
 
 struct AdamEntry {
   void* param;
@@ -177,19 +223,21 @@ struct AdamEntry {
 };
 struct AdamArgs {
   double lr, beta1, beta2;
+  int64_t step;
+  float step_size, inv_root;  // lr / (1 - beta1^step), 1 / sqrt(1 - beta2^step)
   float b1, c1, b2, c2, eps;  // beta, 1 - beta (rounded from fp64)
   float max_norm;
-  int64_t step;
   const float* grad_norm;
   const float* lr_dev;
   const int64_t* step_dev;
 };
-constexpr int kAdamCap = (kParamBytes - 160) / static_cast<int>(sizeof(AdamEntry));
+template <int BYTES>
 struct AdamTable {
+  static constexpr int CAP = (BYTES - 160) / static_cast<int>(sizeof(AdamEntry));
   AdamArgs a;
   uint32_t chunks;
   int count;
-  AdamEntry e[kAdamCap];
+  AdamEntry e[CAP];
 };
 
 __device__ __forceinline__ double int_power(double b, int64_t t) {
@@ -215,16 +263,16 @@ __device__ __forceinline__ uint32_t scale_exponent(uint32_t top) {
   return static_cast<uint32_t>(max(e, 1));
 }
 
-// Largest finite magnitude over the warp's 256 values, as bits (bits of magnitudes order like
-// the magnitudes).
-__device__ __forceinline__ uint32_t warp_top(const float (&v)[8]) {
-  uint32_t top = 0;
+// Largest magnitude over the warp's 256 values, as bits (bits of magnitudes order like the
+// magnitudes); NaN does not count, infinity does unless `finite`.
+__device__ __forceinline__ uint32_t warp_top(const float (&v)[8], bool finite) {
+  float top = 0.0f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const uint32_t b = __float_as_uint(v[j]) & 0x7fffffffu;
-    top = max(top, b < 0x7f800000u ? b : 0u);
+    const float x = fabsf(v[j]);
+    top = fmaxf(top, finite && x > 3.4028235e38f ? 0.0f : x);
   }
-  return __reduce_max_sync(0xffffffffu, top);
+  return __reduce_max_sync(0xffffffffu, __float_as_uint(top));
 }
 
 __device__ __forceinline__ void decode8(uint2 codes, float scale, float (&v)[8]) {
@@ -238,16 +286,13 @@ __device__ __forceinline__ void decode8(uint2 codes, float scale, float (&v)[8])
   }
 }
 
-// Codes of v * inv, rounded to nearest even; what is not finite becomes the NaN code.
-__device__ __forceinline__ uint2 encode8(const float (&v)[8], float inv) {
+// Codes of q (at most 448 in magnitude, or NaN), rounded to nearest even.
+__device__ __forceinline__ uint2 encode8(const float (&q)[8]) {
   uint32_t w[2] = {0, 0};
 #pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    float a = v[2 * h] * inv, b = v[2 * h + 1] * inv;
-    a = (__float_as_uint(a) & 0x7f800000u) == 0x7f800000u ? __uint_as_float(0x7fffffffu) : a;
-    b = (__float_as_uint(b) & 0x7f800000u) == 0x7f800000u ? __uint_as_float(0x7fffffffu) : b;
-    w[h >> 1] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3)) << (16 * (h & 1));
-  }
+  for (int h = 0; h < 4; ++h)
+    w[h >> 1] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(q[2 * h], q[2 * h + 1]), __NV_SATFINITE, __NV_E4M3))
+                 << (16 * (h & 1));
   return make_uint2(w[0], w[1]);
 }
 
@@ -256,8 +301,10 @@ __device__ __forceinline__ uint2 load_codes(const void* base, bool vec, int64_t 
   if (vec && cnt == 8) return *reinterpret_cast<const uint2*>(p);
   uint32_t w[2] = {0, 0};
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (j < cnt) w[j >> 2] |= static_cast<uint32_t>(p[j]) << (8 * (j & 3));
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t code = p[min(j, cnt - 1)];
+    w[j >> 2] |= (j < cnt ? code : 0u) << (8 * (j & 3));
+  }
   return make_uint2(w[0], w[1]);
 }
 
@@ -272,94 +319,198 @@ __device__ __forceinline__ void store_codes(void* base, bool vec, int64_t i, int
     if (j < cnt) p[j] = static_cast<uint8_t>((j < 4 ? c.x : c.y) >> (8 * (j & 3)));
 }
 
-// One AdamW step of 8 elements a thread:
+__device__ __forceinline__ float sqrt_approx(float x) {
+  float y;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+struct AdamScalars {
+  float b1, c1, b2, c2, eps, clip, step_size, inv_root;
+};
+
+// One AdamW step of the 8 elements that a thread holds:
 //   g' = g min(1, max_norm / norm);  m = b1 m + (1 - b1) g';  v = b2 v + (1 - b2) g'^2
 //   p = p (1 - lr decay) - (lr / (1 - b1^t)) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
 // m and v take each product and sum rounded by itself (no contraction): a block's scale then
-// depends on the formula alone, not on how a compiler fuses it.
-__global__ void __launch_bounds__(kThreads, 4) k_adamw(const __grid_constant__ AdamTable t) {
-  grid_dependency_wait();
-  const AdamArgs& a = t.a;
-  __shared__ double s_lr;
-  __shared__ float s_step_size, s_inv_root;
-  if (!step_taken(a.grad_norm)) return;
-  if (threadIdx.x == 0) {
-    const double lr = a.lr_dev ? static_cast<double>(*a.lr_dev) : a.lr;
-    const int64_t step = a.step_dev ? *a.step_dev + 1 : a.step;
-    s_lr = lr;
-    s_step_size = static_cast<float>(lr / (1.0 - int_power(a.beta1, step)));
-    s_inv_root = static_cast<float>(1.0 / sqrt(1.0 - int_power(a.beta2, step)));
-  }
-  __syncthreads();
-  const double lr = s_lr;
-  const float step_size = s_step_size, inv_root = s_inv_root;
-  float clip = 1.0f;
-  if (a.grad_norm && a.max_norm > 0.0f) clip = fminf(1.0f, __fdiv_rn(a.max_norm, *a.grad_norm));
-  const int lane = threadIdx.x & 31;
-
-  const uint32_t c0 = chunk_begin(blockIdx.x, gridDim.x, t.chunks), c1 = chunk_begin(blockIdx.x + 1, gridDim.x, t.chunks);
-  int lo = 0, hi = t.count - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (t.e[mid].chunk0 <= c0) lo = mid;
-    else hi = mid - 1;
-  }
-  for (uint32_t c = c0; c < c1; ++c) {
-    while (lo + 1 < t.count && t.e[lo + 1].chunk0 <= c) ++lo;
-    const AdamEntry& e = t.e[lo];
-    const bool vec = e.flags & kVector, s8 = e.flags & kState8;
-    const int64_t i = static_cast<int64_t>(c - e.chunk0) * kAdamChunk + threadIdx.x * 8;
-    if (i - lane * 8 >= e.n) continue;  // the whole warp lies behind the tensor's end
-    const int cnt = static_cast<int>(max(int64_t(0), min(int64_t(8), e.n - i)));
-    const int64_t block = i / kStateBlock;  // the same for the warp
-    float g[8], p[8], m[8], v[8];
-    load8(e.grad, e.flags & kGradBf16, vec, i, cnt, g);
-    if (e.master) load8(e.master, false, vec, i, cnt, p);
-    else load8(e.param, e.flags & kParamBf16, vec, i, cnt, p);
-    if (s8) {
-      const uint2 mc = load_codes(e.m, vec, i, cnt), vc = load_codes(e.v, vec, i, cnt);
-      decode8(mc, e.m_scale[block], m);
-      decode8(vc, e.v_scale[block], v);
+// depends on the formula alone, not on how a compiler fuses it.  The update's root and quotient
+// come from the MUFU pipe, off by 2^-23 of the update, which leaves the 8-bit step's 60 instructions an
+// element within HBM's time.
+__device__ __forceinline__ void adam8(const AdamScalars& a, float keep, const float (&g)[8], float (&p)[8], float (&m)[8],
+                                      float (&v)[8], float (&root)[8]) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], v[j]);
-    } else {
-      load8(e.m, false, vec, i, cnt, m);
-      load8(e.v, false, vec, i, cnt, v);
-    }
-    const float keep = static_cast<float>(1.0 - lr * e.decay);
-    float root[8];
+  for (int j = 0; j < 8; ++j) {
+    const float gj = __fmul_rn(g[j], a.clip);
+    m[j] = __fadd_rn(__fmul_rn(m[j], a.b1), __fmul_rn(gj, a.c1));
+    v[j] = __fadd_rn(__fmul_rn(v[j], a.b2), __fmul_rn(__fmul_rn(gj, gj), a.c2));
+    root[j] = sqrt_approx(v[j]);
+    p[j] = fmaf(p[j], keep, -a.step_size * m[j] * rcp_approx(fmaf(root[j], a.inv_root, a.eps)));
+  }
+}
+
+// Codes and scales of a block's new moments.
+__device__ __forceinline__ void adam_codes(const float (&m)[8], const float (&v)[8], const float (&root)[8], uint2& mc, uint2& vc,
+                                           float& m_scale, float& v_scale) {
+  uint32_t m_top = warp_top(m, false), v_top = warp_top(v, false);
+  const bool wild = max(m_top, v_top) >= 0x7f800000u;  // an infinity in the block, for the whole warp
+  if (wild) {
+    m_top = warp_top(m, true);
+    v_top = warp_top(v, true);
+  }
+  const uint32_t r_top = __float_as_uint(__fsqrt_rn(__uint_as_float(v_top)));
+  const uint32_t me = scale_exponent(m_top), re = scale_exponent(r_top);
+  m_scale = m_top ? __uint_as_float(me << 23) : 0.0f;
+  v_scale = r_top ? __uint_as_float(re << 23) : 0.0f;
+  const float m_inv = m_top ? __uint_as_float((254u - me) << 23) : 1.0f, r_inv = r_top ? __uint_as_float((254u - re) << 23) : 1.0f;
+  float qm[8], qr[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    qm[j] = m[j] * m_inv;
+    qr[j] = root[j] * r_inv;
+    // A root above zero never becomes zero: m may still be large there, and m / eps would blow the
+    // step up.
+    if (v[j] > 0.0f && qr[j] < 0.001953125f) qr[j] = 0.001953125f;
+  }
+  if (wild) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float gj = __fmul_rn(g[j], clip);
-      m[j] = __fadd_rn(__fmul_rn(m[j], a.b1), __fmul_rn(gj, a.c1));
-      v[j] = __fadd_rn(__fmul_rn(v[j], a.b2), __fmul_rn(__fmul_rn(gj, gj), a.c2));
-      root[j] = __fsqrt_rn(v[j]);
-      p[j] = __fsub_rn(__fmul_rn(p[j], keep), __fmul_rn(step_size, __fdiv_rn(m[j], __fadd_rn(__fmul_rn(root[j], inv_root), a.eps))));
+      if (fabsf(m[j]) > 3.4028235e38f) qm[j] = __uint_as_float(0x7fffffffu);
+      if (v[j] > 3.4028235e38f) qr[j] = __uint_as_float(0x7fffffffu);
     }
-    store8(e.param, e.flags & kParamBf16, vec, i, cnt, p);
-    if (e.master) store8(e.master, false, vec, i, cnt, p);
-    if (s8) {
-      const uint32_t m_top = warp_top(m), r_top = warp_top(root);
-      const uint32_t me = scale_exponent(m_top), re = scale_exponent(r_top);
-      const uint2 mc = encode8(m, m_top ? __uint_as_float((254u - me) << 23) : 1.0f);
-      uint2 vc = encode8(root, r_top ? __uint_as_float((254u - re) << 23) : 1.0f);
-      // A root above zero never becomes zero: m may still be large there, and m / eps would blow
-      // the step up.
+  }
+  mc = encode8(qm);
+  vc = encode8(qr);
+}
+
+// The usual case, 8 elements that exist behind aligned pointers.  The types are template
+// parameters, so that all loads are issued before the first of them is waited for.
+template <uint32_t KIND>
+__device__ __forceinline__ void adam_whole(const AdamEntry& e, const AdamScalars& a, float keep, int64_t i, int lane) {
+  constexpr bool PB = KIND & kParamBf16, GB = KIND & kGradBf16, S8 = KIND & kState8, MASTER = KIND & kMaster;
+  float g[8], p[8], m[8], v[8], root[8];
+  uint2 mc, vc;
+  float m_scale, v_scale;
+  load8(e.grad, GB, true, i, 8, g);
+  if constexpr (MASTER) load8(e.master, false, true, i, 8, p);
+  else load8(e.param, PB, true, i, 8, p);
+  if constexpr (S8) {
+    mc = load_codes(e.m, true, i, 8);
+    vc = load_codes(e.v, true, i, 8);
+    m_scale = e.m_scale[i / kStateBlock];
+    v_scale = e.v_scale[i / kStateBlock];
+    decode8(mc, m_scale, m);
+    decode8(vc, v_scale, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        uint32_t& w = j < 4 ? vc.x : vc.y;
-        if (root[j] > 0.0f && ((w >> (8 * (j & 3))) & 0x7fu) == 0) w |= 1u << (8 * (j & 3));
-      }
-      store_codes(e.m, vec, i, cnt, mc);
-      store_codes(e.v, vec, i, cnt, vc);
-      if (lane == 0) {
-        e.m_scale[block] = m_top ? __uint_as_float(me << 23) : 0.0f;
-        e.v_scale[block] = r_top ? __uint_as_float(re << 23) : 0.0f;
-      }
-    } else {
-      store8(e.m, false, vec, i, cnt, m);
-      store8(e.v, false, vec, i, cnt, v);
+    for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], v[j]);
+  } else {
+    load8(e.m, false, true, i, 8, m);
+    load8(e.v, false, true, i, 8, v);
+  }
+  adam8(a, keep, g, p, m, v, root);
+  store8(e.param, PB, true, i, 8, p);
+  if constexpr (MASTER) store8(e.master, false, true, i, 8, p);
+  if constexpr (S8) {
+    adam_codes(m, v, root, mc, vc, m_scale, v_scale);
+    store_codes(e.m, true, i, 8, mc);
+    store_codes(e.v, true, i, 8, vc);
+    if (lane == 0) {
+      e.m_scale[i / kStateBlock] = m_scale;
+      e.v_scale[i / kStateBlock] = v_scale;
     }
+  } else {
+    store8(e.m, false, true, i, 8, m);
+    store8(e.v, false, true, i, 8, v);
+  }
+}
+
+// A tensor's ragged end, and tensors that are not aligned: any types, `cnt` elements (at most 8; for
+// the lanes behind the end, 0 or less).
+__device__ __noinline__ void adam_ragged(const AdamEntry& e, const AdamScalars& a, float keep, int64_t i, int cnt, int lane) {
+  const bool vec = e.flags & kVector, s8 = e.flags & kState8, pb = e.flags & kParamBf16;
+  const int64_t block = (i - lane * 8) / kStateBlock;
+  float g[8], p[8], m[8], v[8], root[8];
+  load8(e.grad, e.flags & kGradBf16, vec, i, cnt, g);
+  if (e.master) load8(e.master, false, vec, i, cnt, p);
+  else load8(e.param, pb, vec, i, cnt, p);
+  if (s8) {
+    decode8(load_codes(e.m, vec, i, cnt), e.m_scale[block], m);
+    decode8(load_codes(e.v, vec, i, cnt), e.v_scale[block], v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], v[j]);
+  } else {
+    load8(e.m, false, vec, i, cnt, m);
+    load8(e.v, false, vec, i, cnt, v);
+  }
+  adam8(a, keep, g, p, m, v, root);
+  store8(e.param, pb, vec, i, cnt, p);
+  if (e.master) store8(e.master, false, vec, i, cnt, p);
+  if (s8) {
+    uint2 mc, vc;
+    float m_scale, v_scale;
+    adam_codes(m, v, root, mc, vc, m_scale, v_scale);
+    __syncwarp();  // every lane has read the block's old scales
+    store_codes(e.m, vec, i, cnt, mc);
+    store_codes(e.v, vec, i, cnt, vc);
+    if (lane == 0) {
+      e.m_scale[block] = m_scale;
+      e.v_scale[block] = v_scale;
+    }
+  } else {
+    store8(e.m, false, vec, i, cnt, m);
+    store8(e.v, false, vec, i, cnt, v);
+  }
+}
+
+// A CTA takes one chunk: CTAs that start in the chunks' order sweep each array front to back, which
+// HBM rewards (428 us for 103 M bf16 weights with fp32 masters and states, 3.08 GB; a persistent grid
+// that strides over the chunks took 536 us, contiguous ranges 527 us).
+template <int BYTES>
+__global__ void __launch_bounds__(kThreads, 4) k_adamw(const __grid_constant__ AdamTable<BYTES> t) {
+  grid_dependency_wait();
+  if (!step_taken(t.a.grad_norm)) return;
+  double lr = t.a.lr;
+  float step_size = t.a.step_size, inv_root = t.a.inv_root;
+  if (t.a.lr_dev || t.a.step_dev) {  // the schedule lies on the device
+    __shared__ double s_lr;
+    __shared__ float s_step_size, s_inv_root;
+    if (threadIdx.x == 0) {
+      if (t.a.lr_dev) lr = static_cast<double>(*t.a.lr_dev);
+      const int64_t step = t.a.step_dev ? *t.a.step_dev + 1 : t.a.step;
+      s_lr = lr;
+      s_step_size = static_cast<float>(lr / (1.0 - int_power(t.a.beta1, step)));
+      s_inv_root = static_cast<float>(1.0 / sqrt(1.0 - int_power(t.a.beta2, step)));
+    }
+    __syncthreads();
+    lr = s_lr;
+    step_size = s_step_size;
+    inv_root = s_inv_root;
+  }
+  AdamScalars a{t.a.b1, t.a.c1, t.a.b2, t.a.c2, t.a.eps, 1.0f, step_size, inv_root};
+  if (t.a.grad_norm && t.a.max_norm > 0.0f) a.clip = fminf(1.0f, __fdiv_rn(t.a.max_norm, *t.a.grad_norm));
+  const int lane = threadIdx.x & 31;
+
+  const uint32_t c = blockIdx.x;
+  const AdamEntry& e = t.e[tensor_of(t, c, 0)];
+  const float keep = static_cast<float>(1.0 - lr * e.decay);
+  const int64_t i = static_cast<int64_t>(c - e.chunk0) * kAdamChunk + threadIdx.x * 8;
+  const int64_t end = i - lane * 8 + 256;  // of the warp's elements
+  if (end <= e.n && (e.flags & kVector)) {
+    switch (e.flags & 15u) {
+      case 0: adam_whole<0>(e, a, keep, i, lane); break;
+      case kParamBf16: adam_whole<kParamBf16>(e, a, keep, i, lane); break;
+      case kGradBf16: adam_whole<kGradBf16>(e, a, keep, i, lane); break;
+      case kParamBf16 | kGradBf16: adam_whole<kParamBf16 | kGradBf16>(e, a, keep, i, lane); break;
+      case kState8: adam_whole<kState8>(e, a, keep, i, lane); break;
+      case kState8 | kParamBf16: adam_whole<kState8 | kParamBf16>(e, a, keep, i, lane); break;
+      case kState8 | kGradBf16: adam_whole<kState8 | kGradBf16>(e, a, keep, i, lane); break;
+      case kState8 | kParamBf16 | kGradBf16: adam_whole<kState8 | kParamBf16 | kGradBf16>(e, a, keep, i, lane); break;
+      case kMaster | kParamBf16: adam_whole<kMaster | kParamBf16>(e, a, keep, i, lane); break;
+      case kMaster | kParamBf16 | kGradBf16: adam_whole<kMaster | kParamBf16 | kGradBf16>(e, a, keep, i, lane); break;
+      case kMaster | kState8 | kParamBf16: adam_whole<kMaster | kState8 | kParamBf16>(e, a, keep, i, lane); break;
+      default: adam_whole<kMaster | kState8 | kParamBf16 | kGradBf16>(e, a, keep, i, lane); break;
+    }
+  } else if (end - 256 < e.n) {
+    adam_ragged(e, a, keep, i, static_cast<int>(min(int64_t(8), e.n - i)), lane);
   }
 }
 
@@ -410,11 +561,47 @@ dsv4v_status check_tensor(const dsv4v_adamw_tensor& t) {
   return DSV4V_OK;
 }
 
-// Launches k_adamw for the tensors a table holds.
-dsv4v_status launch_adamw(AdamTable& t, int sms, cudaStream_t s) {
-  if (t.count == 0) return DSV4V_OK;
-  const unsigned grid = std::min<unsigned>(t.chunks, 4u * static_cast<unsigned>(sms));
-  return launch_pdl(k_adamw, dim3(grid), dim3(kThreads), 0, s, t) == cudaSuccess ? DSV4V_OK : DSV4V_ERR_CUDA;
+// Takes tensors [i, n) into one table and launches it; returns the first tensor not taken, or -1.
+template <int BYTES>
+int launch_norm(const dsv4v_grad* grads, int i, int n, double* partials, int sms, cudaStream_t s, int* used) {
+  static thread_local NormTable<BYTES> t;
+  t.partials = partials + *used;
+  t.chunks = 0;
+  t.count = 0;
+  for (; i < n && t.count < t.CAP; ++i) {
+    const dsv4v_grad& g = grads[i];
+    if (g.n == 0) continue;
+    t.e[t.count++] = NormEntry{g.data, g.n, t.chunks, (g.dtype == DSV4V_BF16 ? 1u : 0u) | (aligned_to(g.data, 16) ? 2u : 0u)};
+    t.chunks += chunks_of(g.n, kNormChunk);
+  }
+  if (t.count == 0) return i;
+  const unsigned grid = std::min<unsigned>({t.chunks, 4u * static_cast<unsigned>(sms), static_cast<unsigned>(kNormMaxCtas)});
+  if (launch_pdl(k_grad_norm<BYTES>, dim3(grid), dim3(kThreads), 0, s, t) != cudaSuccess) return -1;
+  *used += static_cast<int>(grid);
+  return i;
+}
+
+template <int BYTES>
+int launch_adamw(const AdamArgs& args, const dsv4v_adamw_tensor* tensors, int i, int n, int sms, cudaStream_t s) {
+  static thread_local AdamTable<BYTES> t;
+  t.a = args;
+  t.chunks = 0;
+  t.count = 0;
+  for (; i < n && t.count < t.CAP; ++i) {
+    const dsv4v_adamw_tensor& x = tensors[i];
+    if (x.n == 0) continue;
+    const bool s8 = x.state_bits == 8;
+    const size_t state_align = s8 ? 8 : 16;
+    const bool vec = aligned_to(x.param, 16) && aligned_to(x.grad, 16) && (!x.master || aligned_to(x.master, 16)) &&
+                     aligned_to(x.exp_avg, state_align) && aligned_to(x.exp_avg_sq, state_align);
+    t.e[t.count++] = AdamEntry{x.param, x.grad, x.master, x.exp_avg, x.exp_avg_sq, x.exp_avg_scale, x.exp_avg_sq_scale, x.n,
+                               x.weight_decay, t.chunks,
+                               (x.param_dtype == DSV4V_BF16 ? kParamBf16 : 0u) | (x.grad_dtype == DSV4V_BF16 ? kGradBf16 : 0u) |
+                                   (s8 ? kState8 : 0u) | (x.master ? kMaster : 0u) | (vec ? kVector : 0u)};
+    t.chunks += chunks_of(x.n, kAdamChunk);
+  }
+  if (t.count == 0) return i;
+  return launch_pdl(k_adamw<BYTES>, dim3(t.chunks), dim3(kThreads), 0, s, t) == cudaSuccess ? i : -1;
 }
 
 }  // namespace
@@ -443,22 +630,10 @@ dsv4v_status dsv4v_grad_norm(const dsv4v_grad* grads, int n_tensors, float* norm
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   double* partials = static_cast<double*>(workspace);
   int used = 0;
-  static thread_local NormTable t;
   for (int i = 0; i < n_tensors;) {
-    t.partials = partials + used;
-    t.chunks = 0;
-    t.count = 0;
-    for (; i < n_tensors && t.count < kNormCap; ++i) {
-      const dsv4v_grad& g = grads[i];
-      if (g.n == 0) continue;
-      const uint32_t c = chunks_of(g.n, kNormChunk);
-      t.e[t.count++] = NormEntry{g.data, g.n, t.chunks, (g.dtype == DSV4V_BF16 ? 1u : 0u) | (aligned_to(g.data, 16) ? 2u : 0u)};
-      t.chunks += c;
-    }
-    if (t.count == 0) continue;
-    const unsigned grid = std::min<unsigned>({t.chunks, 4u * static_cast<unsigned>(sms), static_cast<unsigned>(kNormMaxCtas)});
-    if (launch_pdl(k_grad_norm, dim3(grid), dim3(kThreads), 0, s, t) != cudaSuccess) return DSV4V_ERR_CUDA;
-    used += static_cast<int>(grid);
+    i = n_tensors - i <= NormTable<kShortBytes>::CAP ? launch_norm<kShortBytes>(grads, i, n_tensors, partials, sms, s, &used)
+                                                     : launch_norm<kParamBytes>(grads, i, n_tensors, partials, sms, s, &used);
+    if (i < 0) return DSV4V_ERR_CUDA;
   }
   return launch_pdl(k_grad_norm_final, dim3(1), dim3(kThreads), 0, s, static_cast<const double*>(partials), used, norm_out) ==
                  cudaSuccess
@@ -469,7 +644,7 @@ dsv4v_status dsv4v_grad_norm(const dsv4v_grad* grads, int n_tensors, float* norm
 dsv4v_status dsv4v_adamw_step(const dsv4v_adamw_config* cfg, const dsv4v_adamw_tensor* tensors, int n_tensors,
                               const float* grad_norm, const float* lr_dev, int64_t* step_dev, void* stream) {
   if (!cfg || n_tensors < 0 || (n_tensors > 0 && !tensors)) return DSV4V_ERR_INVALID_ARG;
-  if (!(cfg->beta1 >= 0.0 && cfg->beta1 < 1.0) || !(cfg->beta2 >= 0.0 && cfg->beta2 < 1.0) || !(static_cast<float>(cfg->eps) > 0.0f) ||
+  if (!(cfg->beta1 >= 0.0 && cfg->beta1 < 1.0) || !(cfg->beta2 >= 0.0 && cfg->beta2 < 1.0) || !(static_cast<float>(cfg->eps) >= 1.17549435e-38f) ||
       !std::isfinite(static_cast<float>(cfg->eps)) || !std::isfinite(cfg->lr) || !(cfg->max_grad_norm >= 0.0) ||
       !std::isfinite(static_cast<float>(cfg->max_grad_norm)) || (!step_dev && cfg->step < 1) || (cfg->max_grad_norm > 0.0 && !grad_norm))
     return DSV4V_ERR_INVALID_ARG;
@@ -485,39 +660,28 @@ dsv4v_status dsv4v_adamw_step(const dsv4v_adamw_config* cfg, const dsv4v_adamw_t
   int sms = 0;
   if (!query_device(&sms, nullptr)) return DSV4V_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  static thread_local AdamTable t;
-  t.a.lr = cfg->lr;
-  t.a.beta1 = cfg->beta1;
-  t.a.beta2 = cfg->beta2;
-  t.a.b1 = static_cast<float>(cfg->beta1);
-  t.a.c1 = static_cast<float>(1.0 - cfg->beta1);
-  t.a.b2 = static_cast<float>(cfg->beta2);
-  t.a.c2 = static_cast<float>(1.0 - cfg->beta2);
-  t.a.eps = static_cast<float>(cfg->eps);
-  t.a.max_norm = static_cast<float>(cfg->max_grad_norm);
-  t.a.step = cfg->step;
-  t.a.grad_norm = grad_norm;
-  t.a.lr_dev = lr_dev;
-  t.a.step_dev = step_dev;
+  AdamArgs a{};
+  a.lr = cfg->lr;
+  a.beta1 = cfg->beta1;
+  a.beta2 = cfg->beta2;
+  a.step = cfg->step;
+  if (!step_dev) {
+    a.step_size = static_cast<float>(cfg->lr / (1.0 - std::pow(cfg->beta1, static_cast<double>(cfg->step))));
+    a.inv_root = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(cfg->beta2, static_cast<double>(cfg->step))));
+  }
+  a.b1 = static_cast<float>(cfg->beta1);
+  a.c1 = static_cast<float>(1.0 - cfg->beta1);
+  a.b2 = static_cast<float>(cfg->beta2);
+  a.c2 = static_cast<float>(1.0 - cfg->beta2);
+  a.eps = static_cast<float>(cfg->eps);
+  a.max_norm = static_cast<float>(cfg->max_grad_norm);
+  a.grad_norm = grad_norm;
+  a.lr_dev = lr_dev;
+  a.step_dev = step_dev;
   for (int i = 0; i < n_tensors;) {
-    t.chunks = 0;
-    t.count = 0;
-    for (; i < n_tensors && t.count < kAdamCap; ++i) {
-      const dsv4v_adamw_tensor& x = tensors[i];
-      if (x.n == 0) continue;
-      const uint32_t c = chunks_of(x.n, kAdamChunk);
-      const bool s8 = x.state_bits == 8;
-      const size_t state_align = s8 ? 8 : 16;
-      const bool vec = aligned_to(x.param, 16) && aligned_to(x.grad, 16) && (!x.master || aligned_to(x.master, 16)) &&
-                       aligned_to(x.exp_avg, state_align) && aligned_to(x.exp_avg_sq, state_align);
-      t.e[t.count++] = AdamEntry{x.param, x.grad, x.master, x.exp_avg, x.exp_avg_sq, x.exp_avg_scale, x.exp_avg_sq_scale, x.n,
-                                 x.weight_decay, t.chunks,
-                                 (x.param_dtype == DSV4V_BF16 ? kParamBf16 : 0u) | (x.grad_dtype == DSV4V_BF16 ? kGradBf16 : 0u) |
-                                     (s8 ? kState8 : 0u) | (vec ? kVector : 0u)};
-      t.chunks += c;
-    }
-    const dsv4v_status st = launch_adamw(t, sms, s);
-    if (st != DSV4V_OK) return st;
+    i = n_tensors - i <= AdamTable<kShortBytes>::CAP ? launch_adamw<kShortBytes>(a, tensors, i, n_tensors, sms, s)
+                                                     : launch_adamw<kParamBytes>(a, tensors, i, n_tensors, sms, s);
+    if (i < 0) return DSV4V_ERR_CUDA;
   }
   k_adamw_end<<<1, 1, 0, s>>>(step_dev, grad_norm);
   return cudaGetLastError() == cudaSuccess ? DSV4V_OK : DSV4V_ERR_CUDA;

@@ -171,7 +171,7 @@ def _stream(stream):
     if stream is not None:
         return ctypes.c_void_p(stream)
     import torch
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
 def _check(status: int, where: str):
@@ -439,12 +439,13 @@ def _matrix(t, what, rows, cols, ld, layer, device):
     if t is None:
         return None
     import torch
-    if t.dtype != (torch.bfloat16 if layer.dtype == DSV4V_BF16 else torch.float32):
+    if t.dtype is not (torch.bfloat16 if layer.dtype == DSV4V_BF16 else torch.float32):
         raise ValueError(f"{what} is {t.dtype}, the layer is not")
-    if tuple(t.shape) != (rows, cols):
+    if t.shape != (rows, cols):
         raise ValueError(f"{what} has shape {tuple(t.shape)}, not {(rows, cols)}")
-    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) != (ld or cols)):
-        raise ValueError(f"{what} has strides {t.stride()}, not {(ld or cols, 1)}")
+    step = t.stride()
+    if (step[1] != 1 and cols > 1) or (step[0] != (ld or cols) and rows > 1):
+        raise ValueError(f"{what} has strides {step}, not {(ld or cols, 1)}")
     if t.device != device:
         raise ValueError(f"{what} is on {t.device}, not on {device}")
     return t.data_ptr()
