@@ -305,10 +305,10 @@ dsv4v_status gemm(LinearForm form, const void* a, int64_t lda, const void* b, in
   uint32_t* err = nullptr;
   if (!query_device(&sms, &err)) return DSV4V_ERR_CUDA;
   const bool a_mn = form == LINEAR_WEIGHT_GRAD, b_mn = form != LINEAR_FORWARD;
-  const LinearPlan plan = plan_linear(M, N, K, b_mn, sms);
+  const LinearPlan plan = plan_linear(form, M, N, K, sms);
   if (plan.bn == 0) return DSV4V_ERR_UNSUPPORTED;
   CUtensorMap ta, tb;
-  if (!(a_mn ? tensor_map_bf16(a, K, M, linear_box_a(true), lda, &ta) : tensor_map_bf16(a, M, K, linear_box_a(false), lda, &ta)) ||
+  if (!(a_mn ? tensor_map_bf16(a, K, M, linear_box_a(plan, true), lda, &ta) : tensor_map_bf16(a, M, K, linear_box_a(plan, false), lda, &ta)) ||
       !(b_mn ? tensor_map_bf16(b, K, N, linear_box_b(plan, true), ldb, &tb)
              : tensor_map_bf16(b, N, K, linear_box_b(plan, false), ldb, &tb)))
     return DSV4V_ERR_CUDA;
@@ -333,6 +333,12 @@ dsv4v_status forward(const Layer& l, const void* x, const void* w, const float* 
   e.z = static_cast<__nv_bfloat16*>(z);
   e.ld_z = l.ld_z;
   e.act = l.act;
+  if (linear_is_few(l.rows, l.k)) {
+    int sms = 0;
+    if (!query_device(&sms, nullptr)) return DSV4V_ERR_CUDA;
+    return cuda_status(launch_linear_few(x, l.ld_x, w, l.ld_w, static_cast<int>(l.rows), static_cast<int>(l.n), static_cast<int>(l.k), e,
+                                         sms, s));
+  }
   e.vec_io = rows16(y, l.ld_y) && rows16(residual, l.ld_residual) && rows16(z, l.ld_z);
   return gemm(LINEAR_FORWARD, x, l.ld_x, w, l.ld_w, l.rows, l.n, l.k, e, s);
 }

@@ -32,14 +32,22 @@ enum LinearForm {
 
 struct LinearPlan {
   int pair = 0, bn = 0, ks = 1;  // CTA pairs; columns of a tile; K splits (cluster size)
-  int tiles_m = 0, tiles_n = 0, kb_total = 0, grid = 0;
+  int tiles_m = 0, tiles_n = 0, kb_total = 0 /* stages */, grid = 0;
+  int a_rows = 0;                // rows of the boxes of a K-major A
 };
 
 // Tile, pairing and split of D[M, N] over a contraction of K, on `sms` SMs.
-LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool b_mn, int sms);
-// Rows of the boxes of A's and B's tensor maps under a plan (64 for MN-major operands).
-inline int linear_box_a(bool a_mn) { return a_mn ? 64 : 128; }
-inline int linear_box_b(const LinearPlan& p, bool b_mn) { return b_mn ? 64 : (p.pair ? p.bn / 2 : p.bn); }
+LinearPlan plan_linear(LinearForm form, int64_t M, int64_t N, int64_t K, int sms);
+// Depth of a stage, and rows of the boxes of A's and B's tensor maps (for an MN-major operand, rows
+// of the contraction) under a plan.
+inline int linear_depth(const LinearPlan& p) { return p.bn <= 128 ? 128 : 64; }
+inline int linear_box_a(const LinearPlan& p, bool a_mn) { return a_mn ? linear_depth(p) : p.a_rows; }
+inline int linear_box_b(const LinearPlan& p, bool b_mn) { return b_mn ? linear_depth(p) : (p.pair ? p.bn / 2 : p.bn); }
+
+// The forward of a few rows without tensor cores, and whether it is taken.
+bool linear_is_few(int64_t M, int64_t K);
+cudaError_t launch_linear_few(const void* x, int64_t ld_x, const void* w, int64_t ld_w, int M, int N, int K, const LinearEpilogue& e,
+                              int sms, cudaStream_t s);
 
 cudaError_t launch_linear(LinearForm form, const LinearPlan& plan, const CUtensorMap& ta, const CUtensorMap& tb, int M, int N,
                           const LinearEpilogue& e, uint32_t* err, cudaStream_t s);

@@ -7,9 +7,9 @@
 // columns and row strides need not divide into tiles, boxes or vectors.
 //
 // Bounds and tiles.  What an SM takes in limits the main loop before the tensor pipe does: TMA
-// brings about 57 bytes a clock into an SM, and a 128 x N x 64 step needs (128 + N) 128 bytes for
-// 2 N clocks of MMA: 842 against 512 clocks at N = 256.  A pair of CTAs (cta_group::2) shares one B
-// tile, which leaves 575 of 512.  So large products run on pairs; single CTAs serve small ones,
+// brings about 65 bytes a clock into an SM, and a 128 x N x 64 step needs (128 + N) 128 bytes for
+// 2 N clocks of MMA: 750 against 512 clocks at N = 256.  A pair of CTAs (cta_group::2) shares one B
+// tile, which balances the two.  So large products run on pairs; single CTAs serve small ones,
 // split along K over a cluster where there are fewer tiles than SMs.  Each split writes its fp32
 // partial to its own shared memory and finishes a share of the tile, reading the partials of the
 // others through distributed shared memory in rank order: no workspace, no atomics, one result.
@@ -36,26 +36,134 @@ constexpr int kGroupM = 8;                 // row tiles of a raster group
 
 template <int BN, bool PAIR>
 struct Tile {
-  static constexpr int A_BYTES = BM * BK * 2;
+  // A stage holds KPS 64-deep steps: a narrow tile's single step is shorter than the hand-over of a
+  // stage (about 240 clocks) and too few bytes in flight to hide memory.
+  static constexpr int KPS = BN <= 128 ? 2 : 1;
   static constexpr int B_ROWS = PAIR ? BN / 2 : BN;
   static constexpr int B_BYTES = B_ROWS * BK * 2;
-  static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int BUDGET = kMaxDynSmem - 1024 - 256 - kStagingBytes;
-  static constexpr int STAGES = BUDGET / STAGE > 8 ? 8 : BUDGET / STAGE;
-  static constexpr int TMEM_COLS = 2 * BN <= 128 ? 128 : (2 * BN <= 256 ? 256 : 512);
-  static constexpr int OFF_STAGING = STAGES * STAGE;
-  static constexpr int OFF_BARRIERS = OFF_STAGING + kStagingBytes;
-  static constexpr int SMEM = 1024 + OFF_BARRIERS + 256;
+  static constexpr int OFF_BARRIERS = (kMaxDynSmem - 1024 - 512 - kStagingBytes) & ~1023;
+  static constexpr int OFF_STAGING = OFF_BARRIERS + 512;
+  static constexpr int SMEM = 1024 + OFF_STAGING + kStagingBytes;
+  static constexpr int RING = OFF_BARRIERS;
+  static constexpr int TMEM_COLS = 2 * BN <= 128 ? 128 : (2 * BN <= 256 ? 256 : 512);  // two accumulators
   // Row stride, in floats, of a split's fp32 partial in the ring: 16 bytes off a multiple of 128,
   // so that the rows of a warp's 16-byte accesses fall on different banks.
   static constexpr int PART_LD = BN + 4;
-  static_assert(PAIR || BM * PART_LD * 4 <= STAGES * STAGE, "a partial tile has to fit the ring");
+  static_assert(PAIR || BM * PART_LD * 4 <= RING, "a partial tile has to fit the ring");
 };
+constexpr int kMaxStages = 16;
+
+// ---------------------------------------------------------------------------- barriers
+// The load and MMA warps run their loops as whole warps, with one lane issuing: their counters and
+// descriptors then live in uniform registers, which the issued instructions take their operands
+// from.  As one lane's loops they cost 380 and 550 clocks a step, more than a narrow tile's work.
+// Barriers go by their shared-memory address, and the waits are those of common.cuh.
+template <bool CLUSTER>
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  if constexpr (CLUSTER)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+  return ok != 0;
+}
+template <bool CLUSTER>
+__device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint32_t* err, uint32_t code) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (bar_try<CLUSTER>(bar, parity)) return true;
+    if ((i & 255u) == 0) {
+      if (*abort_flag) return false;
+      const uint64_t now = global_timer_ns();
+      if (t0 == 0) {
+        t0 = now;
+      } else if (now - t0 > kWaitLimitNs) {
+        atomicCAS(err, 0u, code);
+        *abort_flag = 1;
+        return false;
+      }
+    }
+  }
+}
+// The whole warp waits for the phase of the given parity and leaves together; false once the wait
+// has given up (see mbar_wait).
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint32_t* err, uint32_t code) {
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i)
+    if (__all_sync(0xffffffffu, bar_try<CLUSTER>(bar, parity))) return true;
+  return __all_sync(0xffffffffu, bar_wait_long<CLUSTER>(bar, parity, abort_flag, err, code));
+}
+
+// The instructions below are executed by a whole, converged warp and issued by one of its lanes
+// (always the same one): the election is part of the instruction's own predicate, not a branch.
+#define ELECTED(body) "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t" body "}"
+
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile(ELECTED("@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t") ::"r"(bar), "r"(bytes) : "memory");
+}
+
+// Tiled load of one box at (x, y) into this CTA's shared memory, counted on the barrier at `bar`
+// (PAIR: a shared::cluster address, the leader's).
+template <bool PAIR>
+__device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+  if constexpr (PAIR)
+    asm volatile(ELECTED("@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+                         " [%0], [%1, {%3, %4}], [%2];\n\t") ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+                 : "memory");
+  else
+    asm volatile(ELECTED("@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                         " [%0], [%1, {%3, %4}], [%2];\n\t") ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+                 : "memory");
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T; PAIR: of both CTAs, M = 256.
+template <bool PAIR>
+__device__ __forceinline__ void mma_step(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (PAIR)
+    asm volatile(ELECTED(".reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                         "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t") ::"r"(d_tmem),
+                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+                 : "memory");
+  else
+    asm volatile(ELECTED(".reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                         "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t") ::"r"(d_tmem),
+                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
+// Arrives on the barrier (PAIR: on both CTAs') when every MMA issued so far has completed.
+template <bool PAIR>
+__device__ __forceinline__ void commit_to(uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile(ELECTED("@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t") ::"r"(bar),
+                 "h"(static_cast<uint16_t>(3))
+                 : "memory");
+  else
+    asm volatile(ELECTED("@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t") ::"r"(bar) : "memory");
+}
 
 struct Params {
   int M, N;              // extents of D
   int tiles_m, tiles_n;  // BM (PAIR: 2 BM) x BN tiles
-  int kb_total;          // 64-deep steps of the contraction
+  int kb_total;          // stages of the contraction, 64 KPS deep
+  int a_rows;            // rows of a K-major A's boxes: fewer than BM where D has fewer (the MMA then
+                         // reads what lies behind them, into accumulator rows that nobody looks at)
+  int stages;            // of the ring
   LinearEpilogue e;
   uint32_t* err;
 };
@@ -156,6 +264,70 @@ __device__ __forceinline__ uint4 pack8(const float* v) {
   return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
 
+// Cluster split-K: this rank's share of a tile.  The tile's 8-column pieces are dealt to the ranks
+// in turn; a piece's partials are all fetched, then summed in rank order.
+template <int BN, bool FWD, int KS>
+__device__ __forceinline__ void finish_pieces(const Params& p, float* part, int slice, int rows, int m0, int n0) {
+  constexpr int PIECES = BN / 8, LD = Tile<BN, false>::PART_LD;
+  const LinearEpilogue& e = p.e;
+  uint32_t base[KS];
+#pragma unroll
+  for (int k = 0; k < KS; ++k) base[k] = mapa_shared(smem_u32(part), static_cast<uint32_t>(k));
+  for (int i = (static_cast<int>(threadIdx.x) - 64) * KS + slice; i < rows * PIECES; i += 32 * kEpiWarps * KS) {
+    const int lr = i / PIECES, c = (i - lr * PIECES) * 8;
+    const int row = m0 + lr, col = n0 + c;
+    if (col >= p.N) continue;
+    const uint32_t at = static_cast<uint32_t>(lr * LD + c) * 4u;
+    float4 q[KS][2];
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      q[k][0] = ld_shared_cluster_f4(base[k] + at);
+      q[k][1] = ld_shared_cluster_f4(base[k] + at + 16);
+    }
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      v[0] += q[k][0].x, v[1] += q[k][0].y, v[2] += q[k][0].z, v[3] += q[k][0].w;
+      v[4] += q[k][1].x, v[5] += q[k][1].y, v[6] += q[k][1].z, v[7] += q[k][1].w;
+    }
+    const int n = min(8, p.N - col);
+    const bool whole = e.vec_io && n == 8;
+    auto put = [&](__nv_bfloat16* dst) {
+      if (whole) {
+        *reinterpret_cast<uint4*>(dst) = pack8(v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < n) dst[j] = __float2bfloat16_rn(v[j]);
+      }
+    };
+    if constexpr (FWD) {
+      if (e.bias) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < n) v[j] += e.bias[col + j];
+      }
+      if (e.z) put(e.z + static_cast<int64_t>(row) * e.ld_z + col);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = activate(v[j], e.act);
+      if (e.residual) {
+        const __nv_bfloat16* r = e.residual + static_cast<int64_t>(row) * e.ld_residual + col;
+        if (whole) {
+          const uint4 w4 = *reinterpret_cast<const uint4*>(r);
+          const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[2 * j] += bf16_lo(w[j]), v[2 * j + 1] += bf16_hi(w[j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < n) v[j] += __bfloat162float(r[j]);
+        }
+      }
+    }
+    put(e.y + static_cast<int64_t>(row) * e.ld_y + col);
+  }
+}
+
 // ---------------------------------------------------------------------------- kernel
 // A_MN / B_MN: the operand is MN-major, loaded as 64 x 64 boxes of its stored [K, MN] matrix (atom
 // columns of 8 KB); else K-major, one box of 64 columns.  FWD: bias, activation, residual and the
@@ -166,13 +338,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     k_linear(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
              const __grid_constant__ Params p, const int ks) {
   using T = Tile<BN, PAIR>;
-  constexpr int STAGES = T::STAGES;
+  constexpr int KPS = T::KPS;
   constexpr int BMT = PAIR ? 2 * BM : BM;
+  // One step's A and B; a stage is KPS A's, then KPS B's.  An MN-major operand's atom columns hold
+  // the stage's whole depth.
+  const uint32_t a_bytes = A_MN ? BM * BK * 2 : static_cast<uint32_t>(p.a_rows) * BK * 2;
+  const uint32_t stage_bytes = KPS * (a_bytes + T::B_BYTES);
+  constexpr uint32_t kAtom = 8192 * KPS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + T::OFF_BARRIERS);
-  uint64_t* empty = full + STAGES;
-  uint64_t* tfull = empty + STAGES;
+  uint64_t* empty = full + kMaxStages;
+  uint64_t* tfull = empty + kMaxStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* mma_done = tempty + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(mma_done + 1);
@@ -190,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tiles = p.tiles_m * p.tiles_n;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
+    for (int s = 0; s < p.stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -232,57 +409,55 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------------ loads
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, issued = 0, issued_phase = 0;
-      bool ok = true;
-      // Both CTAs of a pair complete a stage on the leader's barrier, for which the leader posts
-      // the bytes.
-      const uint32_t full_leader = PAIR ? mapa_shared(smem_u32(full), 0) : 0u;
-      const bool posts = !PAIR || rank == 0;
-      constexpr uint32_t kTx = (PAIR ? 2 : 1) * T::STAGE;
-      auto load = [&](uint8_t* dst, const CUtensorMap* map, int s, int x, int y) {
-        if constexpr (PAIR) tma_load_2d_pair(dst, map, full_leader + 8u * s, x, y);
-        else tma_load_2d(dst, map, &full[s], x, y);
-      };
-      for (int t = t_first; ok && t < tiles; t += t_step) {
-        int mt, nt;
-        tile_at(p, t, mt, nt);
-        const int m0 = mt * BMT + static_cast<int>(rank) * BM;
-        const int n0 = nt * BN + static_cast<int>(rank) * (BN / 2) * (PAIR ? 1 : 0);
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.err, kErrTimeoutProducer)) {
-            ok = false;
-            break;
-          }
-          uint8_t* sa = smem + stage * T::STAGE;
-          uint8_t* sb = sa + T::A_BYTES;
-          if (posts) mbar_arrive_expect_tx(&full[stage], kTx);
+    int stage = 0;
+    uint32_t phase = 0, issued = 0, issued_phase = 0;
+    bool ok = true;
+    // Both CTAs of a pair complete a stage on the leader's barrier, for which the leader posts the
+    // bytes.
+    const uint32_t full_bar = smem_u32(full), empty_bar = smem_u32(empty), ring = smem_u32(smem);
+    const uint32_t full_leader = PAIR ? mapa_shared(full_bar, 0) : full_bar;
+    const bool posts = !PAIR || rank == 0;
+    const uint32_t tx = (PAIR ? 2 : 1) * stage_bytes;
+    for (int t = t_first; t < tiles; t += t_step) {
+      int mt, nt;
+      tile_at(p, t, mt, nt);
+      const int m0 = mt * BMT + static_cast<int>(rank) * BM;
+      const int n0 = nt * BN + static_cast<int>(rank) * (BN / 2) * (PAIR ? 1 : 0);
+      for (int kb = kb0; kb < kb1; ++kb) {
+        ok = ok && bar_wait(empty_bar + 8u * stage, phase ^ 1, abort_flag, p.err, kErrTimeoutProducer);
+        if (ok) {
+          const uint32_t sa = ring + static_cast<uint32_t>(stage) * stage_bytes, sb = sa + KPS * a_bytes, bar = full_leader + 8u * stage;
+          if (posts) bar_expect(full_bar + 8u * stage, tx);
+          const int k0 = kb * (KPS * BK);
           if constexpr (A_MN) {
 #pragma unroll
-            for (int j = 0; j < BM / 64; ++j) load(sa + j * 8192, &tm_a, stage, m0 + 64 * j, kb * BK);
+            for (int j = 0; j < BM / 64; ++j) tma_tile<PAIR>(sa + j * kAtom, &tm_a, bar, m0 + 64 * j, k0);
           } else {
-            load(sa, &tm_a, stage, kb * BK, m0);
+#pragma unroll
+            for (int j = 0; j < KPS; ++j) tma_tile<PAIR>(sa + j * a_bytes, &tm_a, bar, k0 + j * BK, m0);
           }
           if constexpr (B_MN) {
 #pragma unroll
-            for (int j = 0; j < T::B_ROWS / 64; ++j) load(sb + j * 8192, &tm_b, stage, n0 + 64 * j, kb * BK);
+            for (int j = 0; j < T::B_ROWS / 64; ++j) tma_tile<PAIR>(sb + j * kAtom, &tm_b, bar, n0 + 64 * j, k0);
           } else {
-            load(sb, &tm_b, stage, kb * BK, n0);
+#pragma unroll
+            for (int j = 0; j < KPS; ++j) tma_tile<PAIR>(sb + j * T::B_BYTES, &tm_b, bar, k0 + j * BK, n0);
           }
           issued |= 1u << stage;
           issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1;
-          }
+        }
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1;
         }
       }
-      // No copy is in flight when the CTA exits: the MMAs consumed every stage, unless a wait gave
-      // up; then wait for each one here.  The second CTA of a pair has no full barrier of its own
-      // and waits for the MMAs' release of the stages that it filled.
+    }
+    // No copy is in flight when the CTA exits: the MMAs consumed every stage, unless a wait gave
+    // up; then wait for each one here.  The second CTA of a pair has no full barrier of its own
+    // and waits for the MMAs' release of the stages that it filled.
+    if (lane == 0) {
       volatile int never = 0;
-      for (int s = 0; s < STAGES; ++s) {
+      for (int s = 0; s < p.stages; ++s) {
         if (!(issued & (1u << s))) continue;
         mbar_wait(posts ? &full[s] : &empty[s], (issued_phase >> s) & 1u, &never, p.err, kErrTimeoutProducer);
       }
@@ -290,58 +465,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMAs
-    if (lane == 0) {
-      if (PAIR && rank != 0) {
-        volatile int never = 0;  // its TMEM is written until the leader's final commit
-        mbar_wait(mma_done, 0, &never, p.err, kErrTimeoutMma);
-      } else {
-        constexpr uint32_t idesc = idesc_bf16_mn(BMT, BN, A_MN, B_MN);
-        constexpr uint64_t kStepA = A_MN ? 128 : 2, kStepB = B_MN ? 128 : 2;  // 16 of K, in 16-byte units
-        int stage = 0, acc = 0;
-        uint32_t phase = 0, acc_phase = 0;
-        bool ok = true;
-        for (int t = t_first; ok && t < tiles; t += t_step) {
-          const bool free_acc = PAIR ? mbar_wait_cluster(&tempty[acc], acc_phase ^ 1, abort_flag, p.err, kErrTimeoutMma)
-                                     : mbar_wait(&tempty[acc], acc_phase ^ 1, abort_flag, p.err, kErrTimeoutMma);
-          if (!free_acc) break;
+    if (PAIR && rank != 0) {
+      volatile int never = 0;  // its TMEM is written until the leader's final commit
+      mbar_wait(mma_done, 0, &never, p.err, kErrTimeoutMma);
+    } else {
+      constexpr uint32_t idesc = idesc_bf16_mn(BMT, BN, A_MN, B_MN);
+      constexpr uint64_t kStepA = A_MN ? 128 : 2, kStepB = B_MN ? 128 : 2;  // 16 of K, in 16-byte units
+      const uint32_t full_bar = smem_u32(full), empty_bar = smem_u32(empty), tfull_bar = smem_u32(tfull), tempty_bar = smem_u32(tempty);
+      const uint64_t adesc0 = sdesc_sw128(smem_u32(smem), A_MN ? kAtom : 16, 1024);
+      const uint64_t bdesc0 = sdesc_sw128(smem_u32(smem) + KPS * a_bytes, B_MN ? kAtom : 16, 1024);
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int t = t_first; t < tiles; t += t_step) {
+        ok = ok && bar_wait<PAIR>(tempty_bar + 8u * acc, acc_phase ^ 1, abort_flag, p.err, kErrTimeoutMma);
+        tc_fence_after_sync();
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          ok = ok && bar_wait(full_bar + 8u * stage, phase, abort_flag, p.err, kErrTimeoutMma);
           tc_fence_after_sync();
-          const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
-          for (int kb = kb0; kb < kb1; ++kb) {
-            if (!mbar_wait(&full[stage], phase, abort_flag, p.err, kErrTimeoutMma)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after_sync();
-            const uint32_t a_addr = smem_u32(smem + stage * T::STAGE);
-            const uint64_t adesc = sdesc_sw128(a_addr, A_MN ? 8192 : 16, 1024);
-            const uint64_t bdesc = sdesc_sw128(a_addr + T::A_BYTES, B_MN ? 8192 : 16, 1024);
+          const uint32_t at = static_cast<uint32_t>(stage) * (stage_bytes / 16);
+          if (ok) {
 #pragma unroll
-            for (int k = 0; k < BK / 16; ++k) {
-              const uint32_t accum = (kb > kb0 || k > 0) ? 1u : 0u;
-              if constexpr (PAIR) umma_bf16_pair(d_tmem, adesc + kStepA * k, bdesc + kStepB * k, idesc, accum);
-              else umma_bf16(d_tmem, adesc + kStepA * k, bdesc + kStepB * k, idesc, accum);
+            for (int j = 0; j < KPS; ++j) {
+              // a step deeper: the next tile of a K-major operand, 64 rows on in an MN-major one
+              const uint64_t adesc = adesc0 + (at + (A_MN ? j * 512u : j * (a_bytes / 16)));
+              const uint64_t bdesc = bdesc0 + (at + (B_MN ? j * 512u : j * (T::B_BYTES / 16u)));
+#pragma unroll
+              for (int k = 0; k < BK / 16; ++k) {
+                const uint32_t accum = (kb > kb0 || j > 0 || k > 0) ? 1u : 0u;
+                mma_step<PAIR>(d_tmem, adesc + kStepA * k, bdesc + kStepB * k, idesc, accum);
+              }
             }
-            if constexpr (PAIR) umma_commit_pair(&empty[stage]);
-            else umma_commit(&empty[stage]);
-            if (++stage == STAGES) {
-              stage = 0;
-              phase ^= 1;
-            }
+            commit_to<PAIR>(empty_bar + 8u * stage);
           }
-          if (!ok) break;
-          if constexpr (PAIR) umma_commit_pair(&tfull[acc]);
-          else umma_commit(&tfull[acc]);
-          if (++acc == 2) {
-            acc = 0;
-            acc_phase ^= 1;
+          if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1;
           }
         }
-        // Every MMA issued completes before TMEM is released.
-        if constexpr (PAIR) umma_commit_pair(mma_done);
-        else umma_commit(mma_done);
-        volatile int never = 0;
-        mbar_wait(mma_done, 0, &never, p.err, kErrTimeoutMma);
+        if (ok) commit_to<PAIR>(tfull_bar + 8u * acc);
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1;
+        }
       }
+      // Every MMA issued completes before TMEM is released.
+      commit_to<PAIR>(smem_u32(mma_done));
+      volatile int never = 0;
+      mbar_wait(mma_done, 0, &never, p.err, kErrTimeoutMma);
     }
     __syncwarp();
     if (!PAIR && ks > 1) {
@@ -380,7 +552,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (g + 2 < NG) fetch_box(e.residual, e.ld_residual, row0, n0 + 32 * (g + 2), p.M, p.N, e.vec_io, lane, res);
             __syncwarp();
           }
+          float v[32];
           tmem_ld_wait(r);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
           if (g + 2 >= NG) {  // this warp's last read of the accumulator
             tc_fence_before_sync();
             __syncwarp();
@@ -390,9 +565,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           const int col0 = n0 + 32 * g;
-          float v[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
           if constexpr (FWD) {
             if (e.bias) {
               if (col0 + 32 <= p.N) {
@@ -466,70 +638,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int g = half; g < NG; g += 2) {
           uint32_t r[32];
+          float v[32];
           tmem_ld32(t_row + g * 32, r);
           tmem_ld_wait(r);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
           if (quad * 32 + lane < rows) {
             float4* dst = reinterpret_cast<float4*>(part + (quad * 32 + lane) * T::PART_LD + g * 32);
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-              dst[q] = make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]), __uint_as_float(r[4 * q + 2]),
-                                   __uint_as_float(r[4 * q + 3]));
+              dst[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
           }
         }
       }
       __syncwarp();
       cluster_sync();
-      // The tile's 8-column pieces are dealt to the ranks in turn; a piece is summed in rank order.
-      constexpr int PIECES = BN / 8;
-      const uint32_t base = smem_u32(part);
-      for (int i = (static_cast<int>(threadIdx.x) - 64) * ks + slice; i < rows * PIECES; i += 32 * kEpiWarps * ks) {
-        const int lr = i / PIECES, c = (i - lr * PIECES) * 8;
-        const int row = m0 + lr, col = n0 + c;
-        if (col >= p.N) continue;
-        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        const uint32_t at = base + static_cast<uint32_t>(lr * T::PART_LD + c) * 4u;
-#pragma unroll 4
-        for (int k = 0; k < ks; ++k) {
-          const uint32_t remote = mapa_shared(at, static_cast<uint32_t>(k));
-          const float4 a = ld_shared_cluster_f4(remote), b = ld_shared_cluster_f4(remote + 16);
-          v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w, v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
-        }
-        const int n = min(8, p.N - col);
-        const bool whole = e.vec_io && n == 8;
-        auto put = [&](__nv_bfloat16* dst) {
-          if (whole) {
-            *reinterpret_cast<uint4*>(dst) = pack8(v);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (j < n) dst[j] = __float2bfloat16_rn(v[j]);
-          }
-        };
-        if constexpr (FWD) {
-          if (e.bias) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (j < n) v[j] += e.bias[col + j];
-          }
-          if (e.z) put(e.z + static_cast<int64_t>(row) * e.ld_z + col);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = activate(v[j], e.act);
-          if (e.residual) {
-            const __nv_bfloat16* r = e.residual + static_cast<int64_t>(row) * e.ld_residual + col;
-            if (whole) {
-              const uint4 q = *reinterpret_cast<const uint4*>(r);
-              const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j) v[2 * j] += bf16_lo(w[j]), v[2 * j + 1] += bf16_hi(w[j]);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (j < n) v[j] += __bfloat162float(r[j]);
-            }
-          }
-        }
-        put(e.y + static_cast<int64_t>(row) * e.ld_y + col);
-      }
+      if (ks == 2) finish_pieces<BN, FWD, 2>(p, part, slice, rows, m0, n0);
+      else if (ks == 4) finish_pieces<BN, FWD, 4>(p, part, slice, rows, m0, n0);
+      else finish_pieces<BN, FWD, 8>(p, part, slice, rows, m0, n0);
       __syncwarp();
       cluster_sync();  // no CTA leaves while another still reads its partial
     }
@@ -580,41 +706,188 @@ cudaError_t launch_form(const LinearPlan& plan, const CUtensorMap& ta, const CUt
   return cudaErrorInvalidValue;
 }
 
+// ---------------------------------------------------------------------------- a few rows
+// y of a few rows: a warp takes an output feature at a time and streams its weights, 16
+// bytes a lane, against the rows of x in shared memory.  The weights are read once and bound it:
+// 42 MB for one row of 4608 x 4608.  Against the tensor-core kernel on a 128-row tile it needs no
+// TMEM, clusters or partials, whose set-up is as long as the stream of a small layer.
+constexpr int kFewThreads = 256;
+constexpr int kFewSmem = 48 * 1024;
+
+// F features a warp share what it reads of x.
+template <int R, int F>
+__global__ void __launch_bounds__(kFewThreads, 4) k_linear_few(const __nv_bfloat16* x, int64_t ld_x, const __nv_bfloat16* w,
+                                                            int64_t ld_w, int rows, int N, int K, const LinearEpilogue e) {
+  // x in fp32, R rows of k8 pieces of 8; a piece's halves lie in two planes, so that the 16-byte
+  // reads of a warp are contiguous
+  extern __shared__ ulonglong2 sx[];
+  const int lane = threadIdx.x & 31;
+  const int k8 = K / 8, tail = K % 8;  // whole pieces, and elements behind them
+  launch_dependents();
+  const int first = (static_cast<int>(blockIdx.x) * (kFewThreads / 32) + (threadIdx.x >> 5)) * F;
+  constexpr int UN = F == 1 ? 6 : 4;  // pieces of a feature in flight a lane
+  grid_dependency_wait();
+  // The first weights are on their way while x is staged.
+  uint4 q[UN][F];
+  auto fetch = [&](int f, int c) {
+#pragma unroll
+    for (int u = 0; u < UN; ++u)
+#pragma unroll
+      for (int j = 0; j < F; ++j)
+        q[u][j] = reinterpret_cast<const uint4*>(w + static_cast<int64_t>(min(f + j, N - 1)) * ld_w)[c + u * 32];
+  };
+  bool fetched = first < N && lane + (UN - 1) * 32 < k8;
+  if (fetched) fetch(first, lane);
+  for (int i = threadIdx.x; i < R * k8; i += kFewThreads) {
+    const int r = i / k8, c = i - r * k8;
+    const uint4 q = r < rows ? reinterpret_cast<const uint4*>(x + r * ld_x)[c] : make_uint4(0, 0, 0, 0);
+    sx[(2 * r) * k8 + c] = make_ulonglong2(bf16x2_f2(q.x), bf16x2_f2(q.y));
+    sx[(2 * r + 1) * k8 + c] = make_ulonglong2(bf16x2_f2(q.z), bf16x2_f2(q.w));
+  }
+  __syncthreads();
+  const int step = static_cast<int>(gridDim.x) * (kFewThreads / 32) * F;
+  for (int f = first; f < N; f += step) {
+    const uint4* wf[F];
+#pragma unroll
+    for (int j = 0; j < F; ++j) wf[j] = reinterpret_cast<const uint4*>(w + static_cast<int64_t>(min(f + j, N - 1)) * ld_w);
+    uint64_t acc2[F][R] = {};
+    auto piece = [&](const uint4 (&q)[F], int c) {
+      uint64_t w2[F][4];
+#pragma unroll
+      for (int j = 0; j < F; ++j) {
+        w2[j][0] = bf16x2_f2(q[j].x);
+        w2[j][1] = bf16x2_f2(q[j].y);
+        w2[j][2] = bf16x2_f2(q[j].z);
+        w2[j][3] = bf16x2_f2(q[j].w);
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const ulonglong2 lo = sx[(2 * r) * k8 + c], hi = sx[(2 * r + 1) * k8 + c];
+#pragma unroll
+        for (int j = 0; j < F; ++j) {
+          acc2[j][r] = fma2(w2[j][0], lo.x, acc2[j][r]);
+          acc2[j][r] = fma2(w2[j][1], lo.y, acc2[j][r]);
+          acc2[j][r] = fma2(w2[j][2], hi.x, acc2[j][r]);
+          acc2[j][r] = fma2(w2[j][3], hi.y, acc2[j][r]);
+        }
+      }
+    };
+    int c = lane;
+    for (; c + (UN - 1) * 32 < k8; c += UN * 32) {
+      if (!fetched) fetch(f, c);
+      fetched = false;
+#pragma unroll
+      for (int u = 0; u < UN; ++u) piece(q[u], c + u * 32);
+    }
+    for (; c < k8; c += 32) {
+      uint4 one[F];
+#pragma unroll
+      for (int j = 0; j < F; ++j) one[j] = wf[j][c];
+      piece(one, c);
+    }
+    float acc[F][R];
+#pragma unroll
+    for (int j = 0; j < F; ++j)
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float a, b;
+        upk2(acc2[j][r], a, b);
+        acc[j][r] = a + b;
+      }
+    if (lane < tail) {
+#pragma unroll
+      for (int j = 0; j < F; ++j) {
+        const float wv = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(wf[j])[k8 * 8 + lane]);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          if (r < rows) acc[j][r] = fmaf(wv, __bfloat162float(x[r * ld_x + k8 * 8 + lane]), acc[j][r]);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int j = 0; j < F; ++j)
+#pragma unroll
+        for (int r = 0; r < R; ++r) acc[j][r] += __shfl_xor_sync(0xffffffffu, acc[j][r], o);
+    // lane F r + j finishes feature j of row r
+    float v = 0.0f;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int j = 0; j < F; ++j)
+        if (lane == F * r + j) v = acc[j][r];
+    const int row = lane / F, col = f + lane % F;
+    if (row < rows && col < N) {
+      if (e.bias) v += e.bias[col];
+      if (e.z) e.z[row * e.ld_z + col] = __float2bfloat16_rn(v);
+      v = activate(v, e.act);
+      if (e.residual) v += __bfloat162float(e.residual[row * e.ld_residual + col]);
+      e.y[row * e.ld_y + col] = __float2bfloat16_rn(v);
+    }
+  }
+}
+
+template <int R, int F>
+cudaError_t launch_few(const void* x, int64_t ld_x, const void* w, int64_t ld_w, int rows, int N, int K, const LinearEpilogue& e,
+                       int sms, cudaStream_t s) {
+  const int per = kFewThreads / 32 * F, grid = std::min((N + per - 1) / per, sms * 4);
+  return launch_pdl(k_linear_few<R, F>, dim3(grid), dim3(kFewThreads), static_cast<size_t>(R) * (K / 8) * 32, s,
+                    static_cast<const __nv_bfloat16*>(x), ld_x, static_cast<const __nv_bfloat16*>(w), ld_w, rows, N, K, e);
+}
+
 }  // namespace
 
-LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool b_mn, int sms) {
-  // Clocks of one SM, by what bounds it (see the top): a step takes the longer of its intake at 57
-  // bytes a clock and its MMAs at 2 clocks a column; a tile's epilogue about 14 clocks a column,
-  // under the next tile's steps where there is one.
-  constexpr double kIntake = 57.0, kStart = 2500.0, kEpilogue = 14.0;
+// Up to four rows, as long as they fit shared memory and the sharing of x does not cost more than
+// the tensor-core kernel's set-up (1 x 4608 x 4608: 9.5 us against 12.0 us; 2 rows 11.5 against 12.4;
+// 4 rows of 1024 x 2816 4.1 against 5.0, of 2816 x 1024 5.9 against 5.3).
+bool linear_is_few(int64_t M, int64_t K) { return M <= 2 ? M * K * 4 <= kFewSmem : (M <= 4 && K <= 2048); }
+
+cudaError_t launch_linear_few(const void* x, int64_t ld_x, const void* w, int64_t ld_w, int M, int N, int K, const LinearEpilogue& e,
+                              int sms, cudaStream_t s) {
+  if (M == 1) return launch_few<1, 1>(x, ld_x, w, ld_w, M, N, K, e, sms, s);
+  if (M == 2) return launch_few<2, 2>(x, ld_x, w, ld_w, M, N, K, e, sms, s);
+  return launch_few<4, 2>(x, ld_x, w, ld_w, M, N, K, e, sms, s);
+}
+
+LinearPlan plan_linear(LinearForm form, int64_t M, int64_t N, int64_t K, int sms) {
+  // Microseconds, fitted to every tile and split at 25 shapes of each form (1 to 8000 rows, widths 64
+  // to 4608): the plan with the least estimate runs within 1.4% of the fastest one on average, 14% at
+  // worst.  A stage takes the longest of its hand-over, its MMAs and its bytes into the SM; an
+  // epilogue runs under the next tile's stages where there is one; clusters stay inside a GPC, so
+  // that fewer of the larger ones fit (33 of 4 CTAs and 15 of 8, of 148 SMs).
+  constexpr double kStart = 2.75, kHandOver = 0.31, kMma = 0.075, kMmaColumn = 0.001, kBytes = 132e3, kColumn = 0.0123,
+                   kTile = 0.13, kPairTile = 0.8, kSplit = 0.46, kSplitColumn = 0.015, kSplitRank = 0.009;
+  const bool a_mn = form == LINEAR_WEIGHT_GRAD, b_mn = form != LINEAR_FORWARD;
   LinearPlan best;
   double best_cost = 1e300;
-  const int64_t kb = (K + BK - 1) / BK;
   for (int pair = 1; pair >= 0; --pair)
     for (int bn : {256, 192, 128, 64}) {
       if (pair ? (bn == 64 || (bn == 192 && b_mn)) : bn == 192) continue;
-      const int64_t bm = pair ? 2 * BM : BM;
-      const int64_t tm = (M + bm - 1) / bm, tn = (N + bn - 1) / bn, tiles = tm * tn;
+      const int64_t bm = pair ? 2 * BM : BM, tm = (M + bm - 1) / bm, tn = (N + bn - 1) / bn, tiles = tm * tn;
       if (tiles > (int64_t(1) << 30)) continue;
-      const double step = std::max(2.0 * bn, (BM + (pair ? bn / 2 : bn)) * 128 / kIntake);
+      LinearPlan p;
+      p.pair = pair;
+      p.bn = bn;
+      p.a_rows = pair || a_mn ? BM : static_cast<int>(std::min<int64_t>(BM, (M + 7) / 8 * 8));
+      const int steps = linear_depth(p) / BK;
+      const int64_t kb = (K + linear_depth(p) - 1) / linear_depth(p);
+      const double stage = std::max({kHandOver, steps * (kMma + kMmaColumn * bn), steps * (p.a_rows + (pair ? bn / 2 : bn)) * 128 / kBytes});
       for (int ks = 1; ks <= (pair ? 1 : 8); ks *= 2) {
-        if (ks > 1 && (tiles * ks > sms || kb < 2 * ks)) break;
-        const int64_t slots = pair ? sms / 2 : sms / ks;
-        if (slots < 1) break;
+        const int64_t slots = ks == 4 ? sms * 33 / 148 : (ks == 8 ? sms * 15 / 148 : sms / (pair ? 2 : ks));
+        if (slots < 1 || (ks > 1 && (tiles > slots || kb < 2 * ks))) break;
         const int64_t waves = (tiles + slots - 1) / slots;
-        const double main = step * static_cast<double>((kb + ks - 1) / ks);
-        double epilogue = kEpilogue * bn;
-        if (ks > 1) epilogue = 1500.0 + epilogue / 2 + 3.0 * bn;  // to shared memory, barriers, a share of the tile
-        const double cost = kStart + main + (waves - 1) * std::max(main, epilogue) + epilogue;
-        if (cost < best_cost * (1 - 1e-9)) {
+        const double main = stage * static_cast<double>((kb + ks - 1) / ks);
+        double epilogue = kColumn * bn * (form == LINEAR_FORWARD ? 1.0 : 0.7);
+        if (ks > 1) epilogue = kSplit + (kSplitColumn + kSplitRank * ks) * bn * static_cast<double>(std::min<int64_t>(M, BM)) / BM;
+        const double cost = kStart + main + (waves - 1) * (std::max(main, epilogue) + kTile + pair * kPairTile) + epilogue;
+        if (cost < best_cost) {
           best_cost = cost;
-          best.pair = pair;
-          best.bn = bn;
+          best = p;
           best.ks = ks;
           best.tiles_m = static_cast<int>(tm);
           best.tiles_n = static_cast<int>(tn);
           best.kb_total = static_cast<int>(kb);
-          best.grid = static_cast<int>(pair ? 2 * std::min<int64_t>(tiles, slots) : (ks > 1 ? tiles * ks : std::min<int64_t>(tiles, slots)));
+          best.grid = static_cast<int>(pair ? 2 * std::min(tiles, slots) : (ks > 1 ? tiles * ks : std::min(tiles, slots)));
         }
       }
     }
@@ -629,6 +902,10 @@ cudaError_t launch_linear(LinearForm form, const LinearPlan& plan, const CUtenso
   p.tiles_m = plan.tiles_m;
   p.tiles_n = plan.tiles_n;
   p.kb_total = plan.kb_total;
+  p.a_rows = plan.a_rows;
+  const int kps = linear_depth(plan) / BK;
+  const int stage_bytes = kps * ((form == LINEAR_WEIGHT_GRAD ? BM : plan.a_rows) + (plan.pair ? plan.bn / 2 : plan.bn)) * BK * 2;
+  p.stages = std::min(kMaxStages, Tile<256, true>::RING / stage_bytes);
   p.e = e;
   p.err = err;
   switch (form) {
