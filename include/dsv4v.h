@@ -492,7 +492,7 @@ typedef enum {
   DSV4V_ACT_SILU = 2   /* v / (1 + exp(-v)) */
 } dsv4v_activation;
 
-/* rows >= 0 (at most 2^30), widths from 1 to 2^21.  ld_*: row strides in elements, 0 = packed; in
+/* rows >= 0 (at most 2^30), widths from 1 to 2^20.  ld_*: row strides in elements, 0 = packed; in
  * DSV4V_BF16, ld_x and ld_w (0 = in_features) are multiples of 8, else DSV4V_ERR_UNSUPPORTED.
  * dtype is that of x, w, residual, z, y and of their gradients; bias and its gradient are fp32. */
 typedef struct {

@@ -65,7 +65,7 @@ def backward(lib, layer, x=AL, w=2 * AL, z=Z, d_y=Y, dx=DX, dw=DW, db=AL, ws=AL,
 @pytest.mark.parametrize("bad,status", [
     (dict(rows=-1), 1), (dict(rows=(1 << 30) + 1), 1), (dict(in_features=0), 1), (dict(out_features=0), 1),
     (dict(in_features=-5), 1), (dict(activation=3), 1), (dict(activation=-1), 1), (dict(dtype=2), 1),
-    (dict(in_features=(1 << 21) + 8), 2), (dict(out_features=(1 << 21) + 1), 2),
+    (dict(in_features=(1 << 20) + 8), 2), (dict(out_features=(1 << 20) + 1), 2),
     (dict(ld_x=56), 1), (dict(ld_w=56), 1), (dict(ld_y=7), 1), (dict(ld_z=7), 1), (dict(ld_residual=7), 1), (dict(ld_y=-8), 1),
     (dict(ld_x=68), 2), (dict(ld_w=66), 2), (dict(in_features=60), 2), (dict(ld_y=1 << 33), 2)])
 def test_linear_refuses_layers(lib, bad, status):

@@ -1,5 +1,5 @@
-// Entry points of the Linear layer (forward and backward), the kernels around its GEMMs (the
-// gradient of the activation with the bias gradient's sums) and its fp32 CUDA-core path.
+// Entry points of the Linear layer (forward and backward) and the kernels around its products: the
+// gradient of the activation, with the bias gradient's sums.
 #include <algorithm>
 
 #include "common.cuh"
@@ -132,119 +132,12 @@ __global__ void __launch_bounds__(256) k_column_sums(const float* sums, int stri
   out[c] = t;
 }
 
-// ---------------------------------------------------------------------------- fp32 GEMM
-// D[M, N] = A . B^T on CUDA cores (tcgen05 has no exact fp32): 64 x 64 tiles, 16 deep, 4 x 4 outputs a
-// thread.  A_K / B_K: the contraction is the operand's contiguous index; else its M or N index is.
-// Products are summed over 128 of K at a time and these sums added up, which keeps the error near
-// that of sums of 128 + K / 128 terms.
-constexpr int FT = 64, FK = 16, kFlush = 128 / FK;
-
-template <bool K_FAST>
-__device__ __forceinline__ void load_tile(const float* a, int64_t ld, int64_t i0, int64_t n_i, int64_t k0, int64_t n_k,
-                                          float (&q)[4]) {
-  const int t = threadIdx.x;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int64_t i = i0 + (K_FAST ? t / 16 + 16 * j : t % 64), k = k0 + (K_FAST ? t % 16 : t / 64 + 4 * j);
-    q[j] = i < n_i && k < n_k ? a[K_FAST ? i * ld + k : k * ld + i] : 0.0f;
-  }
-}
-template <bool K_FAST>
-__device__ __forceinline__ void stage_tile(float (*s)[FT + 4], const float (&q)[4]) {
-  const int t = threadIdx.x;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (K_FAST) s[t % 16][t / 16 + 16 * j] = q[j];
-    else s[t / 64 + 4 * j][t % 64] = q[j];
-  }
-}
-
-struct EpilogueF32 {
-  float* y;
-  int64_t ld_y;
-  const float* bias;
-  const float* residual;
-  int64_t ld_residual;
-  float* z;
-  int64_t ld_z;
-  int act;
-};
-
-template <bool A_K, bool B_K>
-__global__ void __launch_bounds__(256) k_linear_f32(const float* a, int64_t lda, const float* b,
-                                                    int64_t ldb, int64_t M, int64_t N, int64_t K, const EpilogueF32 e) {
-  launch_dependents();
-  grid_dependency_wait();
-  __shared__ float sa[2][FK][FT + 4], sb[2][FK][FT + 4];
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * FT, n0 = static_cast<int64_t>(blockIdx.y) * FT;
-  float sum[4][4] = {}, part[4][4] = {};
-  float qa[4], qb[4];
-  load_tile<A_K>(a, lda, m0, M, 0, K, qa);
-  load_tile<B_K>(b, ldb, n0, N, 0, K, qb);
-  const int64_t steps = (K + FK - 1) / FK;
-  for (int64_t s = 0; s < steps; ++s) {
-    const int buf = static_cast<int>(s & 1);
-    stage_tile<A_K>(sa[buf], qa);
-    stage_tile<B_K>(sb[buf], qb);
-    __syncthreads();  // one barrier a step: the other buffer's readers passed the last one
-    if (s + 1 < steps) {
-      load_tile<A_K>(a, lda, m0, M, (s + 1) * FK, K, qa);
-      load_tile<B_K>(b, ldb, n0, N, (s + 1) * FK, K, qb);
-    }
-#pragma unroll
-    for (int k = 0; k < FK; ++k) {
-      const float4 av = *reinterpret_cast<const float4*>(&sa[buf][k][ty * 4]);
-      const float4 bv = *reinterpret_cast<const float4*>(&sb[buf][k][tx * 4]);
-      const float am[4] = {av.x, av.y, av.z, av.w}, bn[4] = {bv.x, bv.y, bv.z, bv.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) part[i][j] = fmaf(am[i], bn[j], part[i][j]);
-    }
-    if (s % kFlush == kFlush - 1 || s + 1 == steps) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          sum[i][j] += part[i][j];
-          part[i][j] = 0.0f;
-        }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t r = m0 + ty * 4 + i;
-    if (r >= M) break;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t c = n0 + tx * 4 + j;
-      if (c >= N) break;
-      float v = sum[i][j];
-      if (e.bias) v += e.bias[c];
-      if (e.z) e.z[r * e.ld_z + c] = v;
-      if (e.act == DSV4V_ACT_GELU) v = 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
-      else if (e.act == DSV4V_ACT_SILU) v = v / (1.0f + expf(-v));
-      if (e.residual) v += e.residual[r * e.ld_residual + c];
-      e.y[r * e.ld_y + c] = v;
-    }
-  }
-}
-
-template <bool A_K, bool B_K>
-cudaError_t launch_f32(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t M, int64_t N, int64_t K, const EpilogueF32& e,
-                       cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>((M + FT - 1) / FT), static_cast<unsigned>((N + FT - 1) / FT));
-  return launch_pdl(k_linear_f32<A_K, B_K>, grid, dim3(256), 0, s, static_cast<const float*>(a), lda, static_cast<const float*>(b),
-                    ldb, M, N, K, e);
-}
-
 // ---------------------------------------------------------------------------- host side
 bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 constexpr int64_t kMaxRows = int64_t(1) << 30;
-constexpr int kMaxWidth = 1 << 21;  // 64-column tiles along a grid's y dimension, and tensor-map strides, stay in range
+constexpr int kMaxWidth = 1 << 20;  // 64-column tiles along a grid's y dimension stay in range
 
 struct Layer {
   int64_t rows, k, n, ld_x, ld_w, ld_residual, ld_z, ld_y;
@@ -315,6 +208,15 @@ dsv4v_status gemm(LinearForm form, const void* a, int64_t lda, const void* b, in
   return cuda_status(launch_linear(form, plan, ta, tb, static_cast<int>(M), static_cast<int>(N), e, err, s));
 }
 
+dsv4v_status gemm_f32(LinearForm form, const void* a, int64_t lda, const void* b, int64_t ldb, int64_t M, int64_t N, int64_t K,
+                      const EpilogueF32& e, cudaStream_t s) {
+  int sms = 0;
+  uint32_t* err = nullptr;
+  if (!query_device(&sms, &err)) return DSV4V_ERR_CUDA;
+  return cuda_status(
+      launch_linear_f32(form, static_cast<const float*>(a), lda, static_cast<const float*>(b), ldb, M, N, K, e, err, sms, s));
+}
+
 bool rows16(const void* p, int64_t ld) { return !p || (aligned_to(p, 16) && ld % 8 == 0); }
 
 dsv4v_status forward(const Layer& l, const void* x, const void* w, const float* bias, const void* residual, void* z, void* y,
@@ -322,7 +224,7 @@ dsv4v_status forward(const Layer& l, const void* x, const void* w, const float* 
   if (!l.bf16) {
     const EpilogueF32 e{static_cast<float*>(y), l.ld_y, bias, static_cast<const float*>(residual), l.ld_residual,
                         static_cast<float*>(z), l.ld_z, l.act};
-    return cuda_status(launch_f32<true, true>(x, l.ld_x, w, l.ld_w, l.rows, l.n, l.k, e, s));
+    return gemm_f32(LINEAR_FORWARD, x, l.ld_x, w, l.ld_w, l.rows, l.n, l.k, e, s);
   }
   LinearEpilogue e{};
   e.y = static_cast<__nv_bfloat16*>(y);
@@ -381,12 +283,13 @@ dsv4v_status backward(const Layer& l, const void* x, const void* w, const void* 
     if (dx) {
       e.y = static_cast<float*>(dx);
       e.ld_y = l.ld_x;
-      if (launch_f32<true, false>(dz, ld_dz, w, l.ld_w, l.rows, l.k, l.n, e, s) != cudaSuccess) return DSV4V_ERR_CUDA;
+      const dsv4v_status st = gemm_f32(LINEAR_INPUT_GRAD, dz, ld_dz, w, l.ld_w, l.rows, l.k, l.n, e, s);
+      if (st != DSV4V_OK) return st;
     }
     if (dw) {
       e.y = static_cast<float*>(dw);
       e.ld_y = l.ld_w;
-      if (launch_f32<false, false>(dz, ld_dz, x, l.ld_x, l.n, l.k, l.rows, e, s) != cudaSuccess) return DSV4V_ERR_CUDA;
+      return gemm_f32(LINEAR_WEIGHT_GRAD, dz, ld_dz, x, l.ld_x, l.n, l.k, l.rows, e, s);
     }
     return DSV4V_OK;
   }

@@ -52,4 +52,18 @@ cudaError_t launch_linear_few(const void* x, int64_t ld_x, const void* w, int64_
 cudaError_t launch_linear(LinearForm form, const LinearPlan& plan, const CUtensorMap& ta, const CUtensorMap& tb, int M, int N,
                           const LinearEpilogue& e, uint32_t* err, cudaStream_t s);
 
+// The same for fp32 matrices (linear_f32.cu).
+struct EpilogueF32 {
+  float* y;
+  int64_t ld_y;
+  const float* bias;
+  const float* residual;
+  int64_t ld_residual;
+  float* z;
+  int64_t ld_z;
+  int act;
+};
+cudaError_t launch_linear_f32(LinearForm form, const float* a, int64_t lda, const float* b, int64_t ldb, int64_t M, int64_t N,
+                              int64_t K, const EpilogueF32& e, uint32_t* err, int sms, cudaStream_t s);
+
 }  // namespace dsv4v

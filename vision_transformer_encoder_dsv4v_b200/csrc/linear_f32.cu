@@ -1,0 +1,349 @@
+// The Linear layer's fp32 products on the bf16 tensor cores.
+//
+// A value is the sum of three bf16, x = x0 + x1 + x2 with |x1| <= 2^-8 |x| and |x2| <= 2^-16 |x| (8 bits
+// of its mantissa each), exactly so above 2^-110.  Of the nine products of two values the six largest
+// are formed,
+//   a b = a0 b0 + (a0 b1 + a1 b0) + (a0 b2 + a1 b1 + a2 b0) + O(2^-25 |a b|),
+// in three MMAs, because the parts of B lie behind one another as more columns: a0 meets b0, b1 and
+// b2, a1 meets b0 and b1, a2 meets b0.  The tensor core truncates as it accumulates (2^-23 of the sum
+// an addition): the large products have columns of their own, and every 256 of the contraction all of
+// them are added up in fp32 registers.  The result is about as far from the exact one as an fp32 dot
+// product (2e-7), at 3 bf16 MMAs of 64, 128 and 192 columns in the place of 64 columns of FMAs: 777 x
+// 1001 x 588 takes 13 us, where 4 x 4-output FMA tiles took 46 us, bound by shared-memory reads.
+//
+// Roles (544 threads): warps 0 to 15 load fp32, split it and write the parts into a 3-stage ring
+// (K-major, 128-byte swizzle, transposing where the contraction is not contiguous), and add up the
+// accumulators, 16 columns each; warp 16 issues the MMAs.  All store the 128 x 64 tile at the end.
+// Loading and splitting bounds it, then the MMAs.  Where there are fewer tiles than SMs, two or four
+// CTAs of a cluster share one, each with a part of the contraction; a rank stores its share of the
+// rows and fetches the others' sums through distributed shared memory, in rank order.
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+#include "linear.h"
+
+namespace dsv4v {
+
+namespace {
+
+constexpr int TM = 128, TN = 64, TK = 64;
+constexpr int kConvert = 512, kThreads = kConvert + 32;
+constexpr int kStages = 3;
+constexpr int kFlush = 4;  // stages whose products share an accumulator: 256 of the contraction
+constexpr int kABytes = TM * TK * 2, kBBytes = TN * TK * 2;
+constexpr int kStageBytes = 3 * (kABytes + kBBytes);
+constexpr int kSmem = 1024 + kStages * kStageBytes + 256;
+constexpr int kAccCols = 3 * TN;  // a0 b0 | a0 b1 + a1 b0 + a2 b0 | a0 b2 + a1 b1
+constexpr int kSumLd = TN + 1;
+
+// bf16 parts of eight values, 16 bytes each.  A value that is not finite, or that rounds to a bf16
+// infinity, gives parts that are not finite, and so do the outputs that it enters: those are
+// computed again in fp32 (see the end of the kernel).
+__device__ __forceinline__ void split8(const float (&x)[8], uint4 (&out)[3]) {
+  uint32_t w[3][4];
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    w[0][h] = pack_bf16x2(x[2 * h], x[2 * h + 1]);
+    const float a = x[2 * h] - bf16_lo(w[0][h]), b = x[2 * h + 1] - bf16_hi(w[0][h]);
+    w[1][h] = pack_bf16x2(a, b);
+    w[2][h] = pack_bf16x2(a - bf16_lo(w[1][h]), b - bf16_hi(w[1][h]));
+  }
+#pragma unroll
+  for (int q = 0; q < 3; ++q) out[q] = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
+}
+
+// Row r of A times row c of B, in fp32.
+template <bool A_K, bool B_K>
+__device__ __noinline__ float plain_dot(const float* a, int64_t lda, const float* b, int64_t ldb, int64_t r, int64_t c, int64_t K) {
+  const float* pa = A_K ? a + r * lda : a + r;
+  const float* pb = B_K ? b + c * ldb : b + c;
+  float sum = 0.0f;
+  for (int64_t k0 = 0; k0 < K; k0 += 128) {
+    float part = 0.0f;
+    for (int64_t k = k0; k < min(K, k0 + 128); ++k) part = fmaf(pa[A_K ? k : k * lda], pb[B_K ? k : k * ldb], part);
+    sum += part;
+  }
+  return sum;
+}
+
+// A thread's share of an operand's ROWS x 64 part of a stage, in pieces of one row and eight
+// consecutive contraction indices.
+template <int ROWS, bool K_FAST>
+struct Share {
+  static constexpr int PIECES = ROWS * 8 / kConvert;
+  const float* at[PIECES];  // the first element of the piece in the next stage
+  int64_t ld;
+  int left[PIECES];         // contraction indices from there on (32 bits: at most 2^30 rows, see the limits); 0 outside the rows
+  bool vec;
+  float x[PIECES][8];
+
+  static __device__ __forceinline__ int row(int j) {
+    const int q = static_cast<int>(threadIdx.x) + kConvert * j;
+    return K_FAST ? q / 8 : q % ROWS;
+  }
+  static __device__ __forceinline__ int piece(int j) {
+    const int q = static_cast<int>(threadIdx.x) + kConvert * j;
+    return K_FAST ? q % 8 : q / ROWS;
+  }
+  // Rows i0 .. of n_i, contraction indices k0 .. of n_k.
+  __device__ __forceinline__ Share(const float* a, int64_t ld_, int64_t i0, int64_t n_i, int64_t k0, int64_t n_k) : ld(ld_) {
+    vec = (reinterpret_cast<uintptr_t>(a) & 15) == 0 && ld % 4 == 0;
+#pragma unroll
+    for (int j = 0; j < PIECES; ++j) {
+      const int64_t i = i0 + row(j), k = k0 + piece(j) * 8;
+      at[j] = a + (K_FAST ? i * ld + k : k * ld + i);
+      left[j] = i < n_i ? static_cast<int>(n_k - k) : 0;
+    }
+  }
+  // Starts loading piece j of the next stage.
+  __device__ __forceinline__ void load(int j) {
+    const float* p = at[j];
+    if (left[j] >= 8 && (!K_FAST || vec)) {
+      if constexpr (K_FAST) {
+        const float4 lo = reinterpret_cast<const float4*>(p)[0], hi = reinterpret_cast<const float4*>(p)[1];
+        x[j][0] = lo.x, x[j][1] = lo.y, x[j][2] = lo.z, x[j][3] = lo.w, x[j][4] = hi.x, x[j][5] = hi.y, x[j][6] = hi.z, x[j][7] = hi.w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[j][e] = p[e * ld];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[j][e] = e < left[j] ? p[K_FAST ? e : e * ld] : 0.0f;
+    }
+    at[j] += K_FAST ? TK : TK * ld;
+    left[j] -= TK;
+  }
+  // Its parts into the operand's three tiles.
+  __device__ __forceinline__ void store(int j, uint8_t* tiles) const {
+    uint4 parts[3];
+    split8(x[j], parts);
+    const int r = row(j);
+    uint8_t* to = tiles + r * 128 + ((piece(j) ^ (r & 7)) << 4);
+#pragma unroll
+    for (int q = 0; q < 3; ++q) *reinterpret_cast<uint4*>(to + q * ROWS * TK * 2) = parts[q];
+  }
+};
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* err, uint32_t code) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err, code));
+}
+
+template <bool A_K, bool B_K>
+__global__ void __launch_bounds__(kThreads, 1) k_linear_f32(const float* a, int64_t lda, const float* b, int64_t ldb, int64_t M,
+                                                            int64_t N, int64_t K, const EpilogueF32 e, uint32_t* err, const int ks) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
+  uint64_t* empty = full + kStages;
+  uint64_t* cfull = empty + kStages;   // an accumulator holds its products
+  uint64_t* cempty = cfull + 2;        // it has been added up
+  uint64_t* mma_done = cempty + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(mma_done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], kConvert / 32);
+      mbar_init(&empty[s], 1);
+    }
+    for (int c = 0; c < 2; ++c) {
+      mbar_init(&cfull[c], 1);
+      mbar_init(&cempty[c], kConvert / 32);
+    }
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kConvert / 32) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_holder;
+  if (threadIdx.x == 0) launch_dependents();
+  grid_dependency_wait();
+
+  const int rank = ks > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x / ks) * TM, n0 = static_cast<int64_t>(blockIdx.y) * TN;
+  const int64_t all_stages = (K + TK - 1) / TK, first = all_stages * rank / ks;
+  const int stages = static_cast<int>(all_stages * (rank + 1) / ks - first);  // this rank's
+  float* sums = reinterpret_cast<float*>(smem);  // [TM][kSumLd], once the ring is done with
+  if (warp < kConvert / 32) {
+    // ------------------------------------------------------------------ load and split, add up
+    Share<TM, A_K> pa(a, lda, m0, M, first * TK, K);
+    Share<TN, B_K> pb(b, ldb, n0, N, first * TK, K);
+#pragma unroll
+    for (int j = 0; j < pa.PIECES; ++j) pa.load(j);
+#pragma unroll
+    for (int j = 0; j < pb.PIECES; ++j) pb.load(j);
+    // Rows 32 (warp % 4) + lane, columns 16 (warp / 4) ..
+    const int quad = warp & 3, col = (warp >> 2) * 16;
+    float v[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = 0.0f;
+    const int chunks = (stages + kFlush - 1) / kFlush;
+    int chunk = 0;  // the next one to add up
+    bool ok = true;
+    auto add_up = [&] {
+      const int c = chunk & 1;
+      ok = ok && warp_wait(&cfull[c], static_cast<uint32_t>(chunk >> 1 & 1), abort_flag, err, kErrTimeoutEpilogue);
+      ++chunk;
+      if (!ok) return;
+      tc_fence_after_sync();
+      const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(c * kAccCols + col);
+      uint32_t big[16], mid[16], low[16];
+      tmem_ld16(from, big);
+      tmem_ld16(from + TN, mid);
+      tmem_ld16(from + 2 * TN, low);
+      asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        asm volatile("" : "+r"(big[j]), "+r"(mid[j]), "+r"(low[j]));
+        v[j] += __uint_as_float(big[j]) + (__uint_as_float(mid[j]) + __uint_as_float(low[j]));
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&cempty[c]);
+    };
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int s = 0; s < stages && ok; ++s) {
+      // the accumulator before the present one, once its last MMAs have had a stage's time
+      if (s % kFlush == 1 && s > kFlush) add_up();
+      ok = ok && warp_wait(&empty[stage], phase ^ 1, abort_flag, err, kErrTimeoutProducer);
+      if (!ok) break;
+      uint8_t* to = smem + stage * kStageBytes;
+      // a piece's next loads start as soon as it is split
+#pragma unroll
+      for (int j = 0; j < pa.PIECES; ++j) {
+        pa.store(j, to);
+        pa.load(j);
+      }
+#pragma unroll
+      for (int j = 0; j < pb.PIECES; ++j) {
+        pb.store(j, to + 3 * kABytes);
+        pb.load(j);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[stage]);
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+    while (ok && chunk < chunks) add_up();
+    // The last accumulator is complete, so every MMA has read the ring.
+    if (ok) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) sums[(quad * 32 + lane) * kSumLd + col + j] = v[j];
+    }
+  } else {
+    // ------------------------------------------------------------------ MMAs
+    const uint32_t ring = smem_u32(smem);
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int s = 0; s < stages; ++s) {
+      const int chunk = s / kFlush, c = chunk & 1;
+      if (s % kFlush == 0) ok = ok && warp_wait(&cempty[c], static_cast<uint32_t>(chunk >> 1 & 1) ^ 1u, abort_flag, err, kErrTimeoutMma);
+      ok = ok && warp_wait(&full[stage], phase, abort_flag, err, kErrTimeoutMma);
+      tc_fence_after_sync();
+      if (lane == 0 && ok) {
+        const uint32_t at = ring + static_cast<uint32_t>(stage) * kStageBytes, d = tmem + static_cast<uint32_t>(c * kAccCols);
+        const uint64_t b0 = sdesc_sw128(at + 3 * kABytes, 16, 1024);
+        const uint64_t a0 = sdesc_sw128(at, 16, 1024), a1 = sdesc_sw128(at + kABytes, 16, 1024), a2 = sdesc_sw128(at + 2 * kABytes, 16, 1024);
+#pragma unroll
+        for (int k = 0; k < TK / 16; ++k) {
+          const uint32_t more = s % kFlush != 0 || k > 0 ? 1u : 0u;
+          umma_bf16(d, a0 + 2 * k, b0 + 2 * k, idesc_bf16(TM, 3 * TN, false), more);
+          umma_bf16(d + TN, a1 + 2 * k, b0 + 2 * k, idesc_bf16(TM, 2 * TN, false), 1u);
+          umma_bf16(d + TN, a2 + 2 * k, b0 + 2 * k, idesc_bf16(TM, TN, false), 1u);
+        }
+        umma_commit(&empty[stage]);
+        if (s % kFlush == kFlush - 1 || s + 1 == stages) umma_commit(&cfull[c]);
+      }
+      __syncwarp();
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+    if (lane == 0) {  // every MMA issued completes before TMEM and the ring are given up
+      umma_commit(mma_done);
+      volatile int never = 0;
+      mbar_wait(mma_done, 0, &never, err, kErrTimeoutMma);
+    }
+    __syncwarp();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kConvert / 32) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 512);
+  }
+  if (ks > 1) cluster_sync();  // every rank's sums are in place
+  const int n = static_cast<int>(min(int64_t(TN), N - n0)), rows = static_cast<int>(min(int64_t(TM), M - m0));
+  const int r0 = rows * rank / ks, r1 = rows * (rank + 1) / ks;
+  for (int i = r0 * TN + static_cast<int>(threadIdx.x); i < r1 * TN; i += kThreads) {
+    const int lr = i / TN, lc = i % TN;
+    if (lc >= n) continue;
+    const int64_t r = m0 + lr, c = n0 + lc;
+    float v = sums[lr * kSumLd + lc];
+    if (ks > 1) {
+      const uint32_t at = smem_u32(sums + lr * kSumLd + lc);
+      v = 0.0f;
+      for (int k = 0; k < ks; ++k) v += __uint_as_float(ld_shared_cluster_u32(mapa_shared(at, static_cast<uint32_t>(k))));
+    }
+    // An infinity would meet the zeros among the other operand's parts, or a large value have become
+    // one: the sum of the plain products says what is true.
+    if (!(fabsf(v) <= 3.4028235e38f)) v = plain_dot<A_K, B_K>(a, lda, b, ldb, r, c, K);
+    if (e.bias) v += e.bias[c];
+    if (e.z) e.z[r * e.ld_z + c] = v;
+    if (e.act == DSV4V_ACT_GELU) v = 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+    else if (e.act == DSV4V_ACT_SILU) v = v / (1.0f + expf(-v));
+    if (e.residual) v += e.residual[r * e.ld_residual + c];
+    e.y[r * e.ld_y + c] = v;
+  }
+  if (ks > 1) {
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while another still reads its sums
+  }
+}
+
+template <bool A_K, bool B_K>
+cudaError_t launch(const float* a, int64_t lda, const float* b, int64_t ldb, int64_t M, int64_t N, int64_t K, const EpilogueF32& e,
+                   uint32_t* err, int sms, cudaStream_t s) {
+  auto kern = k_linear_f32<A_K, B_K>;
+  static thread_local uint64_t ready = 0;  // devices on which the shared-memory limit is raised
+  int dev = 0;
+  if (cudaError_t r = cudaGetDevice(&dev)) return r;
+  if (dev >= 64 || !(ready >> dev & 1u)) {
+    if (cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) return r;
+    if (dev < 64) ready |= uint64_t(1) << dev;
+  }
+  const int64_t tm = (M + TM - 1) / TM, tn = (N + TN - 1) / TN, stages = (K + TK - 1) / TK;
+  // The split that leaves no SM a second CTA (33 clusters of four fit 148 SMs), two stages a rank at
+  // least.
+  const int ks = tm * tn * 4 <= sms * 132 / 148 && stages >= 8 ? 4 : (tm * tn * 2 <= sms && stages >= 4 ? 2 : 1);
+  const dim3 grid(static_cast<unsigned>(tm * ks), static_cast<unsigned>(tn));
+  if (ks == 1) return launch_pdl(kern, grid, dim3(kThreads), kSmem, s, a, lda, b, ldb, M, N, K, e, err, 1);
+  return launch_pdl_cluster(kern, grid, dim3(kThreads), kSmem, s, static_cast<unsigned>(ks), a, lda, b, ldb, M, N, K, e, err, ks);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_f32(LinearForm form, const float* a, int64_t lda, const float* b, int64_t ldb, int64_t M, int64_t N,
+                              int64_t K, const EpilogueF32& e, uint32_t* err, int sms, cudaStream_t s) {
+  switch (form) {
+    case LINEAR_FORWARD: return launch<true, true>(a, lda, b, ldb, M, N, K, e, err, sms, s);
+    case LINEAR_INPUT_GRAD: return launch<true, false>(a, lda, b, ldb, M, N, K, e, err, sms, s);
+    case LINEAR_WEIGHT_GRAD: return launch<false, false>(a, lda, b, ldb, M, N, K, e, err, sms, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace dsv4v
