@@ -44,10 +44,13 @@ __device__ __forceinline__ void split8(const float (&x)[8], uint4 (&out)[3]) {
   uint32_t w[3][4];
 #pragma unroll
   for (int h = 0; h < 4; ++h) {
+    float a, b;
     w[0][h] = pack_bf16x2(x[2 * h], x[2 * h + 1]);
-    const float a = x[2 * h] - bf16_lo(w[0][h]), b = x[2 * h + 1] - bf16_hi(w[0][h]);
+    const uint64_t r = sub2(pk2(x[2 * h], x[2 * h + 1]), bf16x2_f2(w[0][h]));
+    upk2(r, a, b);
     w[1][h] = pack_bf16x2(a, b);
-    w[2][h] = pack_bf16x2(a - bf16_lo(w[1][h]), b - bf16_hi(w[1][h]));
+    upk2(sub2(r, bf16x2_f2(w[1][h])), a, b);
+    w[2][h] = pack_bf16x2(a, b);
   }
 #pragma unroll
   for (int q = 0; q < 3; ++q) out[q] = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
@@ -286,27 +289,42 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_f32(const float* a, int6
     tmem_dealloc(tmem, 512);
   }
   if (ks > 1) cluster_sync();  // every rank's sums are in place
-  const int n = static_cast<int>(min(int64_t(TN), N - n0)), rows = static_cast<int>(min(int64_t(TM), M - m0));
-  const int r0 = rows * rank / ks, r1 = rows * (rank + 1) / ks;
-  for (int i = r0 * TN + static_cast<int>(threadIdx.x); i < r1 * TN; i += kThreads) {
-    const int lr = i / TN, lc = i % TN;
-    if (lc >= n) continue;
-    const int64_t r = m0 + lr, c = n0 + lc;
-    float v = sums[lr * kSumLd + lc];
-    if (ks > 1) {
-      const uint32_t at = smem_u32(sums + lr * kSumLd + lc);
-      v = 0.0f;
-      for (int k = 0; k < ks; ++k) v += __uint_as_float(ld_shared_cluster_u32(mapa_shared(at, static_cast<uint32_t>(k))));
+  // A thread stores one column of every eighth row, four at a time: their reads are then in flight
+  // together (element by element, the loop took 4 us of a tile's time).
+  const int rows = static_cast<int>(min(int64_t(TM), M - m0)), r1 = rows * (rank + 1) / ks;
+  const int lc = static_cast<int>(threadIdx.x) % TN;
+  const int64_t col = n0 + lc;
+  if (threadIdx.x < kConvert && col < N) {
+    const float bias = e.bias ? e.bias[col] : 0.0f;
+    constexpr int STEP = kConvert / TN, U = 4;
+    for (int lr = rows * rank / ks + static_cast<int>(threadIdx.x) / TN; lr < r1; lr += STEP * U) {
+      float v[U], res[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int at = min(lr + STEP * u, r1 - 1) * kSumLd + lc;
+        res[u] = e.residual ? e.residual[(m0 + min(lr + STEP * u, r1 - 1)) * e.ld_residual + col] : 0.0f;
+        if (ks == 1) {
+          v[u] = sums[at];
+        } else {
+          v[u] = 0.0f;
+          for (int k = 0; k < ks; ++k)
+            v[u] += __uint_as_float(ld_shared_cluster_u32(mapa_shared(smem_u32(sums + at), static_cast<uint32_t>(k))));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t row = m0 + lr + STEP * u;
+        if (lr + STEP * u >= r1) break;
+        // An infinity would meet the zeros among the other operand's parts, or a large value have
+        // become one: the sum of the plain products says what is true.
+        if (!(fabsf(v[u]) <= 3.4028235e38f)) v[u] = plain_dot<A_K, B_K>(a, lda, b, ldb, row, col, K);
+        float y = v[u] + bias;
+        if (e.z) e.z[row * e.ld_z + col] = y;
+        if (e.act == DSV4V_ACT_GELU) y = 0.5f * y * (1.0f + erff(y * 0.70710678118654752f));
+        else if (e.act == DSV4V_ACT_SILU) y = y / (1.0f + expf(-y));
+        e.y[row * e.ld_y + col] = e.residual ? y + res[u] : y;
+      }
     }
-    // An infinity would meet the zeros among the other operand's parts, or a large value have become
-    // one: the sum of the plain products says what is true.
-    if (!(fabsf(v) <= 3.4028235e38f)) v = plain_dot<A_K, B_K>(a, lda, b, ldb, r, c, K);
-    if (e.bias) v += e.bias[c];
-    if (e.z) e.z[r * e.ld_z + c] = v;
-    if (e.act == DSV4V_ACT_GELU) v = 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
-    else if (e.act == DSV4V_ACT_SILU) v = v / (1.0f + expf(-v));
-    if (e.residual) v += e.residual[r * e.ld_residual + c];
-    e.y[r * e.ld_y + c] = v;
   }
   if (ks > 1) {
     __syncwarp();
