@@ -107,15 +107,16 @@ def test_linear_backward_workspace_size(lib):
 
 
 def test_binding_refuses_shapes_and_types():
-    layer = A.make_linear(4, 64, 8)
-    good = lambda r, c: torch.zeros(r, c, dtype=torch.bfloat16)  # noqa: E731
+    layer, bf16 = A.make_linear(4, 64, 8), torch.bfloat16
+    good = lambda r, c: torch.zeros(r, c, dtype=bf16)  # noqa: E731
+    if not torch.cuda.is_available():  # host tensors, and no device to be the current one
+        assert A._device_index() == -1
+    matrix = lambda t: A._matrix(t, "x", 4, 64, 0, bf16, -1)  # noqa: E731  (host tensors are on "device" -1)
+    assert matrix(good(4, 64)) and matrix(None) is None
+    for bad, match in [(torch.zeros(4, 64), "float32"), (good(4, 63), "shape"), (good(64, 4).t(), "strides"),
+                       (good(4, 72)[:, :64], "strides")]:
+        with pytest.raises(ValueError, match=match):
+            matrix(bad)
     with pytest.raises(ValueError, match="on cpu"):
-        A.dsv4v_linear_forward(layer, good(4, 64), good(8, 64), None, None, None, good(4, 8))
-    with pytest.raises(ValueError, match="not the layer|the layer is not"):
-        A._matrix(torch.zeros(4, 64), "x", 4, 64, 0, layer, torch.device("cpu"))
-    with pytest.raises(ValueError, match="shape"):
-        A._matrix(good(4, 63), "x", 4, 64, 0, layer, torch.device("cpu"))
-    with pytest.raises(ValueError, match="strides"):
-        A._matrix(good(64, 4).t(), "x", 4, 64, 0, layer, torch.device("cpu"))
-    with pytest.raises(ValueError, match="strides"):
-        A._matrix(good(4, 72)[:, :64], "x", 4, 64, 0, layer, torch.device("cpu"))
+        A._matrix(good(4, 64), "x", 4, 64, 0, bf16, 0)
+    assert layer.out_features == 8

@@ -97,14 +97,14 @@ __device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volati
     }
   }
 }
-// The whole warp waits for the phase of the given parity and leaves together; false once the wait
-// has given up (see mbar_wait).
+// Every lane waits for the phase of the given parity; false once the wait has given up (see
+// mbar_wait).  The instructions that follow gather the warp again by their election.
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint32_t* err, uint32_t code) {
 #pragma unroll 1
   for (int i = 0; i < 8; ++i)
-    if (__all_sync(0xffffffffu, bar_try<CLUSTER>(bar, parity))) return true;
-  return __all_sync(0xffffffffu, bar_wait_long<CLUSTER>(bar, parity, abort_flag, err, code));
+    if (bar_try<CLUSTER>(bar, parity)) return true;
+  return bar_wait_long<CLUSTER>(bar, parity, abort_flag, err, code);
 }
 
 // The instructions below are executed by a whole, converged warp and issued by one of its lanes

@@ -434,37 +434,47 @@ def make_linear(rows, in_features, out_features, activation=ACT_NONE, dtype=DSV4
     return Linear(rows, in_features, out_features, activation, dtype, ld_x, ld_w, ld_residual, ld_z, ld_y)
 
 
-def _matrix(t, what, rows, cols, ld, layer, device):
-    """The address of a [rows, cols] matrix of the layer's dtype with row stride ld (0: cols), checked."""
+def _matrix(t, what, rows, cols, ld, dtype, device):
+    """The address of a [rows, cols] matrix with row stride ld (0: cols) on the device of that index, checked."""
     if t is None:
         return None
-    import torch
-    if t.dtype is not (torch.bfloat16 if layer.dtype == DSV4V_BF16 else torch.float32):
-        raise ValueError(f"{what} is {t.dtype}, the layer is not")
+    ld = ld or cols
+    if t.dtype is dtype and t.get_device() == device and t.shape == (rows, cols):
+        step = t.stride()
+        if (step[0] == ld or rows <= 1) and (step[1] == 1 or cols <= 1):
+            return t.data_ptr()
+    if t.get_device() != device:
+        raise ValueError(f"{what} is on {t.device}, the current device is cuda:{device}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{what} is {t.dtype}, the layer is {dtype}")
     if t.shape != (rows, cols):
         raise ValueError(f"{what} has shape {tuple(t.shape)}, not {(rows, cols)}")
-    step = t.stride()
-    if (step[1] != 1 and cols > 1) or (step[0] != (ld or cols) and rows > 1):
-        raise ValueError(f"{what} has strides {step}, not {(ld or cols, 1)}")
-    if t.device != device:
-        raise ValueError(f"{what} is on {t.device}, not on {device}")
-    return t.data_ptr()
+    raise ValueError(f"{what} has strides {t.stride()}, not {(ld, 1)}")
+
+
+def _layer_dtype(layer):
+    import torch
+    return torch.bfloat16 if layer.dtype == DSV4V_BF16 else torch.float32
+
+
+def _raw_stream(stream, device):
+    import torch
+    return stream if stream is not None else torch._C._cuda_getCurrentRawStream(device)
 
 
 def _vector(t, what, n, device):
     import torch
-    return None if t is None else _on_device(t, what, device, (torch.float32,), n)
+    return None if t is None else _on_device(t, what, torch.device("cuda", device), (torch.float32,), n)
 
 
 def dsv4v_linear_forward(layer: Linear, x, w, bias, residual, z, y, stream=None):
     """y = act(x . w^T + bias) + residual; z (the activation's input), bias and residual may be None."""
-    m, k, n, device = layer.rows, layer.in_features, layer.out_features, y.device
-    _current(device, "dsv4v_linear_forward")
-    _check(lib().dsv4v_linear_forward(ctypes.byref(layer), _matrix(x, "x", m, k, layer.ld_x, layer, device),
-                                      _matrix(w, "w", n, k, layer.ld_w, layer, device), _vector(bias, "bias", n, device),
-                                      _matrix(residual, "residual", m, n, layer.ld_residual, layer, device),
-                                      _matrix(z, "z", m, n, layer.ld_z, layer, device),
-                                      _matrix(y, "y", m, n, layer.ld_y, layer, device), _stream(stream)),
+    m, k, n, dtype, device = layer.rows, layer.in_features, layer.out_features, _layer_dtype(layer), _device_index()
+    _check(lib().dsv4v_linear_forward(ctypes.byref(layer), _matrix(x, "x", m, k, layer.ld_x, dtype, device),
+                                      _matrix(w, "w", n, k, layer.ld_w, dtype, device), _vector(bias, "bias", n, device),
+                                      _matrix(residual, "residual", m, n, layer.ld_residual, dtype, device),
+                                      _matrix(z, "z", m, n, layer.ld_z, dtype, device),
+                                      _matrix(y, "y", m, n, layer.ld_y, dtype, device), _raw_stream(stream, device)),
            "dsv4v_linear_forward")
 
 
@@ -474,25 +484,25 @@ def dsv4v_linear_backward_workspace_size(layer: Linear) -> int:
 
 def dsv4v_linear_backward(layer: Linear, x, w, z, d_y, dx, dw, db, workspace, stream=None):
     """dx, dw, db (each may be None) <- the gradients of dsv4v_linear_forward for d_y."""
-    m, k, n, device = layer.rows, layer.in_features, layer.out_features, d_y.device
-    _current(device, "dsv4v_linear_backward")
-    _check(lib().dsv4v_linear_backward(ctypes.byref(layer), _matrix(x, "x", m, k, layer.ld_x, layer, device),
-                                       _matrix(w, "w", n, k, layer.ld_w, layer, device),
-                                       _matrix(z, "z", m, n, layer.ld_z, layer, device),
-                                       _matrix(d_y, "d_y", m, n, layer.ld_y, layer, device),
-                                       _matrix(dx, "dx", m, k, layer.ld_x, layer, device),
-                                       _matrix(dw, "dw", n, k, layer.ld_w, layer, device), _vector(db, "db", n, device),
-                                       *_ws(workspace), _stream(stream)),
+    m, k, n, dtype, device = layer.rows, layer.in_features, layer.out_features, _layer_dtype(layer), _device_index()
+    _check(lib().dsv4v_linear_backward(ctypes.byref(layer), _matrix(x, "x", m, k, layer.ld_x, dtype, device),
+                                       _matrix(w, "w", n, k, layer.ld_w, dtype, device),
+                                       _matrix(z, "z", m, n, layer.ld_z, dtype, device),
+                                       _matrix(d_y, "d_y", m, n, layer.ld_y, dtype, device),
+                                       _matrix(dx, "dx", m, k, layer.ld_x, dtype, device),
+                                       _matrix(dw, "dw", n, k, layer.ld_w, dtype, device), _vector(db, "db", n, device),
+                                       *_ws(workspace), _raw_stream(stream, device)),
            "dsv4v_linear_backward")
 
 
 # ------------------------------------------------------------------------------ optimizer step
 def _dtype_code(t, what):
     import torch
-    code = {torch.float32: DSV4V_F32, torch.bfloat16: DSV4V_BF16}.get(t.dtype)
-    if code is None:
-        raise ValueError(f"{what} is {t.dtype}: fp32 or bf16 is wanted")
-    return code
+    if t.dtype is torch.bfloat16:
+        return DSV4V_BF16
+    if t.dtype is torch.float32:
+        return DSV4V_F32
+    raise ValueError(f"{what} is {t.dtype}: fp32 or bf16 is wanted")
 
 
 def _on_device(t, what, device, dtypes=None, numel=None):
@@ -508,14 +518,27 @@ def _on_device(t, what, device, dtypes=None, numel=None):
     return t.data_ptr()
 
 
-def _current(device, where):
+def _device_index():
+    """The current CUDA device's index (-1 without one)."""
     import torch
-    if device is None:
-        return
-    if device.type != "cuda":
-        raise ValueError(f"{where}: the tensors are on {device}")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"{where}: the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else (torch.cuda.current_device() if torch.cuda.is_available() else -1)
+
+
+def _current(table, where):
+    """The current device's index, which has to be that of the table's tensors."""
+    device = _device_index()
+    if table.index is not None and table.index != device:
+        raise ValueError(f"{where}: the tensors are on cuda:{table.index}, the current device is cuda:{device}")
+    return device
+
+
+def _value(t, what, dtype, device):
+    """The address of a single value on the device of that index, checked."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.get_device() == device and t.numel() == 1:
+        return t.data_ptr()
+    raise ValueError(f"{what} is {t.dtype} [{t.numel()}] on {t.device}: one {dtype} value on cuda:{device} is wanted")
 
 
 class GradTable:
@@ -525,6 +548,7 @@ class GradTable:
     def __init__(self, grads):
         self.tensors = list(grads)
         self.device = self.tensors[0].device if self.tensors else None
+        self.index = self.device.index if self.tensors else None
         self.n = len(self.tensors)
         self.c = (Grad * max(1, self.n))()
         for i, g in enumerate(self.tensors):
@@ -539,9 +563,9 @@ def dsv4v_grad_norm_workspace_size(table) -> int:
 def dsv4v_grad_norm(table: GradTable, norm_out, workspace, stream=None):
     """norm_out (one fp32 value on the device) <- the norm over every gradient of the table."""
     import torch
-    _current(table.device, "dsv4v_grad_norm")
-    out = _on_device(norm_out, "norm_out", table.device or norm_out.device, (torch.float32,), 1)
-    _check(lib().dsv4v_grad_norm(table.c, table.n, out, *_ws(workspace), _stream(stream)), "dsv4v_grad_norm")
+    device = _current(table, "dsv4v_grad_norm")
+    _check(lib().dsv4v_grad_norm(table.c, table.n, _value(norm_out, "norm_out", torch.float32, device), *_ws(workspace),
+                                 _raw_stream(stream, device)), "dsv4v_grad_norm")
 
 
 def make_adamw(lr, beta1=0.9, beta2=0.999, eps=1e-8, step=1, max_grad_norm=0.0) -> AdamwConfig:
@@ -561,32 +585,35 @@ class AdamwTable:
         self.tensors = [dict(t) for t in tensors]
         self.n = len(self.tensors)
         self.device = self.tensors[0]["param"].device if self.n else None
+        self.index = self.device.index if self.n else None
         self.c = (AdamwTensor * max(1, self.n))()
         f32, codes, written = (torch.float32,), (torch.uint8, torch.float8_e4m3fn), []
+        any_float = (torch.float32, torch.bfloat16)
         for i, t in enumerate(self.tensors):
-            p, g = t["param"], t["grad"]
-            n = p.numel()
-            eight = t["exp_avg"].dtype in codes
+            n, eight = t["param"].numel(), t["exp_avg"].dtype in codes
             blocks = (n + DSV4V_STATE_BLOCK - 1) // DSV4V_STATE_BLOCK
-            want = {"param": (None, n), "grad": (None, n), "master": (f32, n),
-                    "exp_avg": (codes if eight else f32, n), "exp_avg_sq": (codes if eight else f32, n),
-                    "exp_avg_scale": (f32, blocks), "exp_avg_sq_scale": (f32, blocks)}
-            ptr = dict.fromkeys(want)
-            for key, (dtypes, numel) in want.items():
+            state = codes if eight else f32
+
+            def address(key, dtypes, numel, optional=False):
                 x = t.get(key)
                 if x is None:
-                    if key == "master" or (key.endswith("scale") and not eight):
-                        continue
+                    if optional:
+                        return None
                     raise ValueError(f"tensors[{i}] has no {key}")
-                if key.endswith("scale") and not eight:
-                    raise ValueError(f"tensors[{i}] has {key}, but fp32 states")
-                ptr[key] = _on_device(x, f"tensors[{i}] {key}", self.device, dtypes, numel)
-                if key != "grad" and x.numel():
-                    written.append((x.data_ptr(), x.data_ptr() + x.numel() * x.element_size(), i))
-            self.c[i] = AdamwTensor(ptr["param"], ptr["grad"], ptr["master"], ptr["exp_avg"], ptr["exp_avg_sq"],
-                                    ptr["exp_avg_scale"], ptr["exp_avg_sq_scale"], n,
-                                    _dtype_code(p, f"tensors[{i}] param"), _dtype_code(g, f"tensors[{i}] grad"),
-                                    8 if eight else 32, float(t.get("weight_decay") or 0.0))
+                ptr = _on_device(x, f"tensors[{i}] {key}", self.device, dtypes, numel)
+                if numel and key != "grad":
+                    written.append((ptr, ptr + numel * x.element_size(), i))
+                return ptr
+
+            if not eight and (t.get("exp_avg_scale") is not None or t.get("exp_avg_sq_scale") is not None):
+                raise ValueError(f"tensors[{i}] has scales, but fp32 states")
+            self.c[i] = AdamwTensor(address("param", any_float, n), address("grad", any_float, n),
+                                    address("master", f32, n, optional=True), address("exp_avg", state, n),
+                                    address("exp_avg_sq", state, n),
+                                    address("exp_avg_scale", f32, blocks) if eight else None,
+                                    address("exp_avg_sq_scale", f32, blocks) if eight else None, n,
+                                    _dtype_code(t["param"], "param"), _dtype_code(t["grad"], "grad"), 8 if eight else 32,
+                                    float(t.get("weight_decay") or 0.0))
         written.sort()
         for (_, end, i), (begin, _, j) in zip(written, written[1:]):
             if begin < end:
@@ -597,12 +624,11 @@ def dsv4v_adamw_step(cfg: AdamwConfig, table: AdamwTable, grad_norm=None, lr_dev
     """One AdamW step of every tensor of the table.  grad_norm, lr_dev: one fp32 value on the
     device; step_dev: one int64 value on the device, advanced by the call."""
     import torch
-    _current(table.device, "dsv4v_adamw_step")
-    args = []
-    for what, t, dtype in (("grad_norm", grad_norm, torch.float32), ("lr_dev", lr_dev, torch.float32),
-                           ("step_dev", step_dev, torch.int64)):
-        args.append(None if t is None else _on_device(t, what, table.device or t.device, (dtype,), 1))
-    _check(lib().dsv4v_adamw_step(ctypes.byref(cfg), table.c, table.n, *args, _stream(stream)), "dsv4v_adamw_step")
+    device = _current(table, "dsv4v_adamw_step")
+    _check(lib().dsv4v_adamw_step(ctypes.byref(cfg), table.c, table.n, _value(grad_norm, "grad_norm", torch.float32, device),
+                                  _value(lr_dev, "lr_dev", torch.float32, device),
+                                  _value(step_dev, "step_dev", torch.int64, device), _raw_stream(stream, device)),
+           "dsv4v_adamw_step")
 
 
 def dsv4v_device_error(stream=None) -> int:
