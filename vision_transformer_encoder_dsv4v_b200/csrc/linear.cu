@@ -193,7 +193,7 @@ dsv4v_status cuda_status(cudaError_t e) { return e == cudaSuccess ? DSV4V_OK : D
 // One bf16 GEMM of the layer: D[M, N] over a contraction of K.  a is stored [M, K] or, for the
 // weight gradient, [K, M]; b is stored [N, K] in the forward, else [K, N].
 dsv4v_status gemm(LinearForm form, const void* a, int64_t lda, const void* b, int64_t ldb, int64_t M, int64_t N, int64_t K,
-                  const LinearEpilogue& e, cudaStream_t s) {
+                  const LinearEpilogue& e, cudaStream_t s, const ColumnSums& cs = ColumnSums()) {
   int sms = 0;
   uint32_t* err = nullptr;
   if (!query_device(&sms, &err)) return DSV4V_ERR_CUDA;
@@ -205,7 +205,7 @@ dsv4v_status gemm(LinearForm form, const void* a, int64_t lda, const void* b, in
       !(b_mn ? tensor_map_bf16(b, K, N, linear_box_b(plan, true), ldb, &tb)
              : tensor_map_bf16(b, N, K, linear_box_b(plan, false), ldb, &tb)))
     return DSV4V_ERR_CUDA;
-  return cuda_status(launch_linear(form, plan, ta, tb, static_cast<int>(M), static_cast<int>(N), e, err, s));
+  return cuda_status(launch_linear(form, plan, ta, tb, static_cast<int>(M), static_cast<int>(N), e, cs, err, s));
 }
 
 dsv4v_status gemm_f32(LinearForm form, const void* a, int64_t lda, const void* b, int64_t ldb, int64_t M, int64_t N, int64_t K,
@@ -266,13 +266,14 @@ dsv4v_status backward(const Layer& l, const void* x, const void* w, const void* 
   const bool products = dx || dw;
   const bool own_dz = l.act != DSV4V_ACT_NONE || (l.bf16 && !rows16(d_y, l.ld_y));
   const bool write_dz = products && own_dz;
+  const int strips = dz_strips(l, sms);
+  const bool sums_in_gemm = l.bf16 && dw && db;  // the weight gradient's kernel adds the strips up
   if (write_dz || db) {
-    const int strips = dz_strips(l, sms);
     float* sums = db ? reinterpret_cast<float*>(ws + bl.sums) : nullptr;
     void* dz = write_dz ? ws + bl.dz : nullptr;
     const cudaError_t e = l.bf16 ? launch_dz<__nv_bfloat16>(l, d_y, z, dz, sums, strips, s) : launch_dz<float>(l, d_y, z, dz, sums, strips, s);
     if (e != cudaSuccess) return DSV4V_ERR_CUDA;
-    if (db && launch_pdl(k_column_sums, dim3(static_cast<unsigned>((l.n + 31) / 32)), dim3(256), 0, s, static_cast<const float*>(sums),
+    if (db && !sums_in_gemm && launch_pdl(k_column_sums, dim3(static_cast<unsigned>((l.n + 31) / 32)), dim3(256), 0, s, static_cast<const float*>(sums),
                          strips, static_cast<int>(l.n), db) != cudaSuccess)
       return DSV4V_ERR_CUDA;
   }
@@ -305,7 +306,9 @@ dsv4v_status backward(const Layer& l, const void* x, const void* w, const void* 
     e.y = static_cast<__nv_bfloat16*>(dw);
     e.ld_y = l.ld_w;
     e.vec_io = rows16(dw, l.ld_w);
-    return gemm(LINEAR_WEIGHT_GRAD, dz, ld_dz, x, l.ld_x, l.n, l.k, l.rows, e, s);
+    ColumnSums cs;
+    if (sums_in_gemm) cs = ColumnSums{reinterpret_cast<const float*>(ws + bl.sums), strips, db};
+    return gemm(LINEAR_WEIGHT_GRAD, dz, ld_dz, x, l.ld_x, l.n, l.k, l.rows, e, s, cs);
   }
   return DSV4V_OK;
 }

@@ -24,6 +24,13 @@ struct LinearEpilogue {
   bool vec_io;                     // the rows of y, residual and z are 16-byte aligned
 };
 
+// out[f] = the sum over strips of sums[strip][f], f < M; out NULL: none.
+struct ColumnSums {
+  const float* sums = nullptr;
+  int strips = 0;
+  float* out = nullptr;
+};
+
 enum LinearForm {
   LINEAR_FORWARD,      // D[rows, out] = x . W^T: both operands K-major
   LINEAR_INPUT_GRAD,   // dx[rows, in] = dz . W: dz K-major, W MN-major
@@ -50,7 +57,7 @@ cudaError_t launch_linear_few(const void* x, int64_t ld_x, const void* w, int64_
                               int sms, cudaStream_t s);
 
 cudaError_t launch_linear(LinearForm form, const LinearPlan& plan, const CUtensorMap& ta, const CUtensorMap& tb, int M, int N,
-                          const LinearEpilogue& e, uint32_t* err, cudaStream_t s);
+                          const LinearEpilogue& e, const ColumnSums& cs, uint32_t* err, cudaStream_t s);
 
 // The same for fp32 matrices (linear_f32.cu).
 struct EpilogueF32 {

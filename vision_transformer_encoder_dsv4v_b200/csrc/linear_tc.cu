@@ -165,6 +165,7 @@ struct Params {
                          // reads what lies behind them, into accumulator rows that nobody looks at)
   int stages;            // of the ring
   LinearEpilogue e;
+  ColumnSums cs;         // weight gradient: the bias gradient that goes with it
   uint32_t* err;
 };
 
@@ -262,6 +263,17 @@ __device__ __forceinline__ void store_box(__nv_bfloat16* dst, int64_t ld, int ro
 
 __device__ __forceinline__ uint4 pack8(const float* v) {
   return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+
+// The bias gradient of rows m0 .. m0 + 127 of dW: the strips' sums, in order.  The epilogue warps have
+// the time of a tile's main loop for it.
+__device__ __forceinline__ void sum_columns(const Params& p, int m0) {
+  const int t = static_cast<int>(threadIdx.x) - 64, f = m0 + t;
+  if (t >= BM || f >= p.M) return;
+  float sum = 0.0f;
+#pragma unroll 8
+  for (int i = 0; i < p.cs.strips; ++i) sum += p.cs.sums[static_cast<int64_t>(i) * p.M + f];
+  p.cs.out[f] = sum;
 }
 
 // Cluster split-K: this rank's share of a tile.  The tile's 8-column pieces are dealt to the ranks
@@ -536,6 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tile_at(p, t, mt, nt);
         const int row0 = mt * BMT + static_cast<int>(rank) * BM + quad * 32;
         const int n0 = nt * BN;
+        if (A_MN && p.cs.out && nt == 0) sum_columns(p, mt * BMT + static_cast<int>(rank) * BM);
         uint4 res[4];
         if (FWD && e.residual) fetch_box(e.residual, e.ld_residual, row0, n0 + 32 * half, p.M, p.N, e.vec_io, lane, res);
         const bool got = mbar_wait(&tfull[acc], acc_phase, abort_flag, p.err, kErrTimeoutEpilogue);
@@ -629,6 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tile_at(p, t_first, mt, nt);
       const int m0 = mt * BM, n0 = nt * BN;
       const int rows = min(BM, p.M - m0);
+      if (A_MN && p.cs.out && nt == 0 && slice == 0) sum_columns(p, m0);
       const bool got = mbar_wait(&tfull[0], 0, abort_flag, p.err, kErrTimeoutEpilogue);
       const bool all_got = __all_sync(0xffffffffu, got);
       tc_fence_after_sync();
@@ -895,8 +909,9 @@ LinearPlan plan_linear(LinearForm form, int64_t M, int64_t N, int64_t K, int sms
 }
 
 cudaError_t launch_linear(LinearForm form, const LinearPlan& plan, const CUtensorMap& ta, const CUtensorMap& tb, int M, int N,
-                          const LinearEpilogue& e, uint32_t* err, cudaStream_t s) {
+                          const LinearEpilogue& e, const ColumnSums& cs, uint32_t* err, cudaStream_t s) {
   Params p{};
+  p.cs = cs;
   p.M = M;
   p.N = N;
   p.tiles_m = plan.tiles_m;
