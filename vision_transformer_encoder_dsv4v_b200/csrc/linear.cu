@@ -15,10 +15,11 @@ namespace {
 // ---------------------------------------------------------------------------- activation gradient
 // dz = dy act'(z).  The bf16 path takes its exponentials and reciprocals from the MUFU pipe (a few
 // 2^-23, against the 2^-9 of the bf16 result); the fp32 path calls erff and expf.
-__device__ __forceinline__ float derivative(float z, int act, bool exact) {
-  if (act == DSV4V_ACT_GELU) {
+template <int ACT, bool EXACT>
+__device__ __forceinline__ float derivative(float z) {
+  if constexpr (ACT == DSV4V_ACT_GELU) {
     // Phi(z) + z phi(z)
-    if (exact)
+    if constexpr (EXACT)
       return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) + z * expf(-0.5f * z * z) * 0.39894228040143268f;
     // erfc by Abramowitz and Stegun 7.1.26, |error| <= 1.5e-7; its e^(-z^2 / 2) serves phi too
     const float t = rcp_approx(fmaf(0.3275911f * 0.70710678118654752f, fabsf(z), 1.0f));
@@ -30,33 +31,39 @@ __device__ __forceinline__ float derivative(float z, int act, bool exact) {
     const float tail = 0.5f * q * t * ex;
     return fmaf(z * 0.39894228040143268f, ex, z >= 0.0f ? 1.0f - tail : tail);
   }
-  if (act == DSV4V_ACT_SILU) {
+  if constexpr (ACT == DSV4V_ACT_SILU) {
     // s (1 + z (1 - s)), s the logistic of z; far below zero s vanishes before z (1 - s) grows
-    const float s = exact ? 1.0f / (1.0f + expf(-z)) : rcp_approx(1.0f + ex2_approx(z * -1.4426950408889634f));
+    const float s = EXACT ? 1.0f / (1.0f + expf(-z)) : rcp_approx(1.0f + ex2_approx(z * -1.4426950408889634f));
     return s * fmaf(z, 1.0f - s, 1.0f);
   }
   return 1.0f;
 }
 
-__device__ __forceinline__ void get8(const __nv_bfloat16* p, bool whole, int cnt, float (&v)[8]) {
-  if (whole) {
-    const uint4 q = *reinterpret_cast<const uint4*>(p);
+// Eight elements of a row: 16-byte pieces as they are loaded, and their values.
+template <class T>
+struct Eight;
+template <>
+struct Eight<__nv_bfloat16> {
+  uint4 q;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { q = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
     v[0] = bf16_lo(q.x), v[1] = bf16_hi(q.x), v[2] = bf16_lo(q.y), v[3] = bf16_hi(q.y);
     v[4] = bf16_lo(q.z), v[5] = bf16_hi(q.z), v[6] = bf16_lo(q.w), v[7] = bf16_hi(q.w);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = j < cnt ? __bfloat162float(p[j]) : 0.0f;
   }
-}
-__device__ __forceinline__ void get8(const float* p, bool whole, int cnt, float (&v)[8]) {
-  if (whole) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+};
+template <>
+struct Eight<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = j < cnt ? p[j] : 0.0f;
   }
-}
+};
+__device__ __forceinline__ float value_of(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float value_of(float x) { return x; }
 // dz lies in the workspace, its rows padded to 8 elements: whole pieces always fit.
 __device__ __forceinline__ void put8(__nv_bfloat16* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) =
@@ -71,34 +78,56 @@ constexpr int kDzCols = 256;  // columns of a CTA: 32 threads of 8, by 8 rows at
 
 // One pass over dy (and z): writes dz where it is wanted and, per strip of rows, the column sums of
 // the unrounded dz, whose strips k_column_sums adds in order.  HBM bounds it.
-template <class T>
-__global__ void __launch_bounds__(256) k_linear_dz(const T* dy, int64_t ld_dy, const T* z, int64_t ld_z,
-                                                   int act, T* dz, int64_t ld_dz, float* sums,
-                                                   int64_t rows, int n, int64_t strip, bool vec) {
+template <class T, int ACT>
+__global__ void __launch_bounds__(256) k_linear_dz(const T* dy, int64_t ld_dy, const T* z, int64_t ld_z, T* dz, int64_t ld_dz,
+                                                   float* sums, int64_t rows, int n, int64_t strip, bool vec) {
   launch_dependents();
   grid_dependency_wait();
-  constexpr bool exact = sizeof(T) == 4;
   __shared__ float s[8][kDzCols + 8];
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
   const int col = blockIdx.x * kDzCols + cx * 8;
   const int cnt = min(8, n - col);
-  const bool whole = vec && cnt == 8;
   float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   if (cnt > 0) {
-    const int64_t r1 = min(rows, static_cast<int64_t>(blockIdx.y + 1) * strip);
-#pragma unroll 2
-    for (int64_t r = static_cast<int64_t>(blockIdx.y) * strip + ry; r < r1; r += 8) {
-      float g[8];
-      get8(dy + r * ld_dy + col, whole, cnt, g);
-      if (act != DSV4V_ACT_NONE) {
-        float v[8];
-        get8(z + r * ld_z + col, whole, cnt, v);
+    const int64_t r0 = static_cast<int64_t>(blockIdx.y) * strip, r1 = min(rows, r0 + strip);
+    auto finish = [&](int64_t r, float (&g)[8], const float (&v)[8]) {
+      if constexpr (ACT != DSV4V_ACT_NONE) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] *= derivative(v[j], act, exact);
+        for (int j = 0; j < 8; ++j) g[j] *= derivative<ACT, sizeof(T) == 4>(v[j]);
       }
       if (dz) put8(dz + r * ld_dz + col, g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[j] += g[j];
+    };
+    int64_t r = r0 + ry;
+    if (vec && cnt == 8) {
+      constexpr int U = 4;  // rows in flight
+      for (; r + 8 * (U - 1) < r1; r += 8 * U) {
+        Eight<T> qg[U], qv[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          qg[u].load(dy + (r + 8 * u) * ld_dy + col);
+          if constexpr (ACT != DSV4V_ACT_NONE) qv[u].load(z + (r + 8 * u) * ld_z + col);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float g[8], v[8] = {};
+          qg[u].values(g);
+          if constexpr (ACT != DSV4V_ACT_NONE) qv[u].values(v);
+          finish(r + 8 * u, g, v);
+        }
+      }
+    }
+    for (; r < r1; r += 8) {
+      float g[8], v[8] = {};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int at = col + min(j, cnt - 1);
+        g[j] = value_of(dy[r * ld_dy + at]);
+        if constexpr (ACT != DSV4V_ACT_NONE) v[j] = value_of(z[r * ld_z + at]);
+        if (j >= cnt) g[j] = 0.0f;
+      }
+      finish(r, g, v);
     }
   }
   if (!sums) return;
@@ -245,14 +274,21 @@ dsv4v_status forward(const Layer& l, const void* x, const void* w, const float* 
   return gemm(LINEAR_FORWARD, x, l.ld_x, w, l.ld_w, l.rows, l.n, l.k, e, s);
 }
 
+template <class T, int ACT>
+cudaError_t launch_dz_act(const Layer& l, const void* d_y, const void* z, void* dz, float* sums, int strips, cudaStream_t s) {
+  const int64_t strip = (l.rows + strips - 1) / strips;
+  const bool vec = aligned_to(d_y, 16) && l.ld_y * sizeof(T) % 16 == 0 &&
+                   (ACT == DSV4V_ACT_NONE || (aligned_to(z, 16) && l.ld_z * sizeof(T) % 16 == 0));
+  return launch_pdl(k_linear_dz<T, ACT>, dim3(static_cast<unsigned>((l.n + kDzCols - 1) / kDzCols), static_cast<unsigned>(strips)),
+                    dim3(256), 0, s, static_cast<const T*>(d_y), l.ld_y, static_cast<const T*>(z), l.ld_z, static_cast<T*>(dz),
+                    dz_ld(l), sums, l.rows, static_cast<int>(l.n), strip, vec);
+}
+
 template <class T>
 cudaError_t launch_dz(const Layer& l, const void* d_y, const void* z, void* dz, float* sums, int strips, cudaStream_t s) {
-  const int64_t strip = (l.rows + strips - 1) / strips;
-  const bool act = l.act != DSV4V_ACT_NONE;
-  const bool vec = aligned_to(d_y, 16) && l.ld_y * sizeof(T) % 16 == 0 && (!act || (aligned_to(z, 16) && l.ld_z * sizeof(T) % 16 == 0));
-  return launch_pdl(k_linear_dz<T>, dim3(static_cast<unsigned>((l.n + kDzCols - 1) / kDzCols), static_cast<unsigned>(strips)),
-                    dim3(256), 0, s, static_cast<const T*>(d_y), l.ld_y, static_cast<const T*>(z), l.ld_z, l.act,
-                    static_cast<T*>(dz), dz_ld(l), sums, l.rows, static_cast<int>(l.n), strip, vec);
+  if (l.act == DSV4V_ACT_GELU) return launch_dz_act<T, DSV4V_ACT_GELU>(l, d_y, z, dz, sums, strips, s);
+  if (l.act == DSV4V_ACT_SILU) return launch_dz_act<T, DSV4V_ACT_SILU>(l, d_y, z, dz, sums, strips, s);
+  return launch_dz_act<T, DSV4V_ACT_NONE>(l, d_y, z, dz, sums, strips, s);
 }
 
 dsv4v_status backward(const Layer& l, const void* x, const void* w, const void* z, const void* d_y, void* dx, void* dw, float* db,
