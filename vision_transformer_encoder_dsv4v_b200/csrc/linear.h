@@ -47,7 +47,7 @@ struct LinearPlan {
 LinearPlan plan_linear(LinearForm form, int64_t M, int64_t N, int64_t K, int sms);
 // Depth of a stage, and rows of the boxes of A's and B's tensor maps (for an MN-major operand, rows
 // of the contraction) under a plan.
-inline int linear_depth(const LinearPlan& p) { return p.bn <= 128 ? 128 : 64; }
+inline int linear_depth(const LinearPlan& p) { return p.bn <= 192 ? 128 : 64; }
 inline int linear_box_a(const LinearPlan& p, bool a_mn) { return a_mn ? linear_depth(p) : p.a_rows; }
 inline int linear_box_b(const LinearPlan& p, bool b_mn) { return b_mn ? linear_depth(p) : (p.pair ? p.bn / 2 : p.bn); }
 

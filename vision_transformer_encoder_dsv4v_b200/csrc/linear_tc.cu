@@ -31,14 +31,15 @@ constexpr int BK = 64;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kMaxDynSmem = 232448;        // 227 KB per CTA
-constexpr int kStagingBytes = kEpiWarps * 2048;  // per epilogue warp: 32 rows x 64 bytes
+constexpr int kBoxBytes = 2048, kBiasBytes = 512;  // per epilogue warp: 32 rows x 64 bytes, and the bias of 4 x 32 columns
+constexpr int kStagingBytes = kEpiWarps * (kBoxBytes + kBiasBytes);
 constexpr int kGroupM = 8;                 // row tiles of a raster group
 
 template <int BN, bool PAIR>
 struct Tile {
   // A stage holds KPS 64-deep steps: a narrow tile's single step is shorter than the hand-over of a
   // stage (about 240 clocks) and too few bytes in flight to hide memory.
-  static constexpr int KPS = BN <= 128 ? 2 : 1;
+  static constexpr int KPS = BN <= 192 ? 2 : 1;
   static constexpr int B_ROWS = PAIR ? BN / 2 : BN;
   static constexpr int B_BYTES = B_ROWS * BK * 2;
   static constexpr int OFF_BARRIERS = (kMaxDynSmem - 1024 - 512 - kStagingBytes) & ~1023;
@@ -538,7 +539,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int half = (warp - 2) >> 2;    // column groups half, half + 2, ...
     const LinearEpilogue& e = p.e;
     constexpr int NG = BN / 32;
-    uint8_t* box = smem + T::OFF_STAGING + (warp - 2) * 2048;
+    uint8_t* box = smem + T::OFF_STAGING + (warp - 2) * kBoxBytes;
+    float* bias_s = reinterpret_cast<float*>(smem + T::OFF_STAGING + kEpiWarps * kBoxBytes + (warp - 2) * kBiasBytes);
     const uint32_t tempty_leader = PAIR ? mapa_shared(smem_u32(tempty), 0) : 0u;
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -551,6 +553,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (A_MN && p.cs.out && nt == 0) sum_columns(p, mt * BMT + static_cast<int>(rank) * BM);
         uint4 res[4];
         if (FWD && e.residual) fetch_box(e.residual, e.ld_residual, row0, n0 + 32 * half, p.M, p.N, e.vec_io, lane, res);
+        if (FWD && e.bias) {  // this warp's columns, under the main loop
+#pragma unroll
+          for (int g = half; g < NG; g += 2) {
+            const int c = n0 + 32 * g + lane;
+            bias_s[16 * (g - half) + lane] = c < p.N ? e.bias[c] : 0.0f;
+          }
+          __syncwarp();
+        }
         const bool got = mbar_wait(&tfull[acc], acc_phase, abort_flag, p.err, kErrTimeoutEpilogue);
         if (!__all_sync(0xffffffffu, got)) break;
         tc_fence_after_sync();
@@ -580,16 +590,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int col0 = n0 + 32 * g;
           if constexpr (FWD) {
             if (e.bias) {
-              if (col0 + 32 <= p.N) {
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                  const float4 b = reinterpret_cast<const float4*>(e.bias + col0)[q];
-                  v[4 * q] += b.x, v[4 * q + 1] += b.y, v[4 * q + 2] += b.z, v[4 * q + 3] += b.w;
-                }
-              } else {
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (col0 + j < p.N) v[j] += e.bias[col0 + j];
+              for (int q = 0; q < 8; ++q) {
+                const float4 b = reinterpret_cast<const float4*>(bias_s + 16 * (g - half))[q];
+                v[4 * q] += b.x, v[4 * q + 1] += b.y, v[4 * q + 2] += b.z, v[4 * q + 3] += b.w;
               }
             }
             uint4 own_res[4];
@@ -865,12 +869,13 @@ cudaError_t launch_linear_few(const void* x, int64_t ld_x, const void* w, int64_
 
 LinearPlan plan_linear(LinearForm form, int64_t M, int64_t N, int64_t K, int sms) {
   // Microseconds, fitted to every tile and split at 25 shapes of each form (1 to 8000 rows, widths 64
-  // to 4608): the plan with the least estimate runs within 1.4% of the fastest one on average, 14% at
+  // to 4608): the plan with the least estimate runs within 0.6% of the fastest one on average, 11% at
   // worst.  A stage takes the longest of its hand-over, its MMAs and its bytes into the SM; an
   // epilogue runs under the next tile's stages where there is one; clusters stay inside a GPC, so
   // that fewer of the larger ones fit (33 of 4 CTAs and 15 of 8, of 148 SMs).
-  constexpr double kStart = 2.75, kHandOver = 0.31, kMma = 0.075, kMmaColumn = 0.001, kBytes = 132e3, kColumn = 0.0123,
-                   kTile = 0.13, kPairTile = 0.8, kSplit = 0.46, kSplitColumn = 0.015, kSplitRank = 0.009;
+  constexpr double kStart = 1.8, kPairStart = 0.87, kHandOver = 0.314, kMma = 0.035, kMmaColumn = 0.0011, kBytes = 132e3,
+                   kEpilogue = 0.27, kColumn = 0.0207, kPlainColumn = 0.0074, kTile = 0.22, kPairTile = 0.75, kSplit = 1.48,
+                   kSplitColumn = 0.0145, kSplitRank = 0.009;
   const bool a_mn = form == LINEAR_WEIGHT_GRAD, b_mn = form != LINEAR_FORWARD;
   LinearPlan best;
   double best_cost = 1e300;
@@ -891,9 +896,9 @@ LinearPlan plan_linear(LinearForm form, int64_t M, int64_t N, int64_t K, int sms
         if (slots < 1 || (ks > 1 && (tiles > slots || kb < 2 * ks))) break;
         const int64_t waves = (tiles + slots - 1) / slots;
         const double main = stage * static_cast<double>((kb + ks - 1) / ks);
-        double epilogue = kColumn * bn * (form == LINEAR_FORWARD ? 1.0 : 0.7);
+        double epilogue = kEpilogue + (form == LINEAR_FORWARD ? kColumn : kPlainColumn) * bn;
         if (ks > 1) epilogue = kSplit + (kSplitColumn + kSplitRank * ks) * bn * static_cast<double>(std::min<int64_t>(M, BM)) / BM;
-        const double cost = kStart + main + (waves - 1) * (std::max(main, epilogue) + kTile + pair * kPairTile) + epilogue;
+        const double cost = kStart + pair * kPairStart + main + (waves - 1) * (std::max(main, epilogue) + kTile + pair * kPairTile) + epilogue;
         if (cost < best_cost) {
           best_cost = cost;
           best = p;
