@@ -113,10 +113,19 @@ def test_linear_forward(rows, k, n, act):
     run_forward("bf16", rows, k, n, act)
 
 
-@pytest.mark.parametrize("rows,k,n", [(1, 1, 1), (1, 300, 5), (63, 17, 65), (64, 16, 64), (130, 588, 97), (777, 588, 201)])
+@pytest.mark.parametrize("rows,k,n", [(1, 1, 1), (1, 300, 5), (63, 17, 65), (64, 16, 64), (130, 588, 97), (777, 588, 201), (6, 1100, 60),
+                                      (300, 300, 130), (129, 256, 64), (5, 257, 1000)])
 @pytest.mark.parametrize("act", ["none", "gelu", "silu"])
 def test_linear_forward_fp32(rows, k, n, act):
     run_forward("f32", rows, k, n, act)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [1, 2, 3, 4, 5])
+@pytest.mark.parametrize("k,n", [(1, 1), (7, 300), (200, 9), (1033, 77), (2048, 130), (4608, 64), (13000, 33)])
+def test_linear_forward_of_a_few_rows(kind, rows, k, n):
+    # the weight-streaming kernels: extents that leave lanes, warps and pieces without work, and lengths behind their limit
+    run_forward(kind, rows, k, n, "gelu")
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
@@ -230,7 +239,8 @@ def test_linear_backward(rows, k, n, act):
     run_backward("bf16", rows, k, n, act)
 
 
-@pytest.mark.parametrize("rows,k,n", [(1, 1, 1), (1, 300, 5), (63, 17, 65), (64, 16, 64), (130, 588, 97), (777, 588, 201)])
+@pytest.mark.parametrize("rows,k,n", [(1, 1, 1), (1, 300, 5), (63, 17, 65), (64, 16, 64), (130, 588, 97), (777, 588, 201), (1100, 60, 6),
+                                      (300, 130, 300), (257, 64, 1000)])
 @pytest.mark.parametrize("act", ["none", "gelu", "silu"])
 def test_linear_backward_fp32(rows, k, n, act):
     run_backward("f32", rows, k, n, act)
@@ -249,6 +259,29 @@ def test_linear_backward_each_gradient_alone(kind, act, want):
                                                   (3000, 72, 1153, 1160, 0), (3000, 71, 1160, 1161, 5)])
 def test_linear_backward_strides(kind, act, rows, k, n, ld_y, offset):
     run_backward(kind, rows, k, n, act, ld_x=pad8(k) + 16, ld_w=pad8(k) + 8, ld_y=ld_y, offset=offset)
+
+
+def test_linear_fp32_values_that_bf16_cannot_hold():
+    # the fp32 products go through bf16 parts: the largest finite values, infinities and NaN come out as in fp32
+    rows, k, n = 40, 100, 70
+    x, w = normal((rows, k), 1.0, torch.float32, 1), normal((n, k), 1.0, torch.float32, 2)
+    big = torch.finfo(torch.float32).max
+    x[3], w[5] = 0.0, 0.0
+    x[3, 7], w[5, 9] = big, -big           # rounds to a bf16 infinity
+    x[8, 1], x[9, 2], x[10, 4] = float("inf"), float("nan"), -float("inf")
+    w[20, 1] = 0.0                          # infinity times zero
+    x[11], x[12] = 1e-30, 1e30
+    want = np64(x) @ np64(w).T
+    y = torch.empty(rows, n, device="cuda")
+    A.dsv4v_linear_forward(A.make_linear(rows, k, n, dtype=A.DSV4V_F32), x, w, None, None, None, y)
+    got = np64(y)
+    over = np.abs(want) > big
+    want = np.where(over & np.isfinite(want), np.sign(want) * np.inf, want)
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    assert np.array_equal(got[np.isinf(want)], want[np.isinf(want)])
+    ok = np.isfinite(want)
+    terms = np.abs(np.nan_to_num(np64(x), posinf=0, neginf=0)) @ np.abs(np64(w)).T
+    close(got[ok], want[ok], (accumulate("f32", k, terms) + 2.0 ** -24 * np.abs(np.nan_to_num(want)))[ok], "y")
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f32"])

@@ -238,12 +238,12 @@ dsv4v_status gemm(LinearForm form, const void* a, int64_t lda, const void* b, in
 }
 
 dsv4v_status gemm_f32(LinearForm form, const void* a, int64_t lda, const void* b, int64_t ldb, int64_t M, int64_t N, int64_t K,
-                      const EpilogueF32& e, cudaStream_t s) {
+                      const EpilogueF32& e, cudaStream_t s, const ColumnSums& cs = ColumnSums()) {
   int sms = 0;
   uint32_t* err = nullptr;
   if (!query_device(&sms, &err)) return DSV4V_ERR_CUDA;
   return cuda_status(
-      launch_linear_f32(form, static_cast<const float*>(a), lda, static_cast<const float*>(b), ldb, M, N, K, e, err, sms, s));
+      launch_linear_f32(form, static_cast<const float*>(a), lda, static_cast<const float*>(b), ldb, M, N, K, e, cs, err, sms, s));
 }
 
 bool rows16(const void* p, int64_t ld) { return !p || (aligned_to(p, 16) && ld % 8 == 0); }
@@ -303,7 +303,7 @@ dsv4v_status backward(const Layer& l, const void* x, const void* w, const void* 
   const bool own_dz = l.act != DSV4V_ACT_NONE || (l.bf16 && !rows16(d_y, l.ld_y));
   const bool write_dz = products && own_dz;
   const int strips = dz_strips(l, sms);
-  const bool sums_in_gemm = l.bf16 && dw && db;  // the weight gradient's kernel adds the strips up
+  const bool sums_in_gemm = dw && db;  // the weight gradient's kernel adds the strips up
   if (write_dz || db) {
     float* sums = db ? reinterpret_cast<float*>(ws + bl.sums) : nullptr;
     void* dz = write_dz ? ws + bl.dz : nullptr;
@@ -313,6 +313,8 @@ dsv4v_status backward(const Layer& l, const void* x, const void* w, const void* 
                          strips, static_cast<int>(l.n), db) != cudaSuccess)
       return DSV4V_ERR_CUDA;
   }
+  ColumnSums cs;
+  if (sums_in_gemm) cs = ColumnSums{reinterpret_cast<const float*>(ws + bl.sums), strips, db};
   const void* dz = write_dz ? static_cast<const void*>(ws + bl.dz) : d_y;
   const int64_t ld_dz = write_dz ? dz_ld(l) : l.ld_y;
   if (!l.bf16) {
@@ -326,7 +328,7 @@ dsv4v_status backward(const Layer& l, const void* x, const void* w, const void* 
     if (dw) {
       e.y = static_cast<float*>(dw);
       e.ld_y = l.ld_w;
-      return gemm_f32(LINEAR_WEIGHT_GRAD, dz, ld_dz, x, l.ld_x, l.n, l.k, l.rows, e, s);
+      return gemm_f32(LINEAR_WEIGHT_GRAD, dz, ld_dz, x, l.ld_x, l.n, l.k, l.rows, e, s, cs);
     }
     return DSV4V_OK;
   }
@@ -342,8 +344,6 @@ dsv4v_status backward(const Layer& l, const void* x, const void* w, const void* 
     e.y = static_cast<__nv_bfloat16*>(dw);
     e.ld_y = l.ld_w;
     e.vec_io = rows16(dw, l.ld_w);
-    ColumnSums cs;
-    if (sums_in_gemm) cs = ColumnSums{reinterpret_cast<const float*>(ws + bl.sums), strips, db};
     return gemm(LINEAR_WEIGHT_GRAD, dz, ld_dz, x, l.ld_x, l.n, l.k, l.rows, e, s, cs);
   }
   return DSV4V_OK;

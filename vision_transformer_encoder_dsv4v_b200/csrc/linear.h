@@ -71,6 +71,6 @@ struct EpilogueF32 {
   int act;
 };
 cudaError_t launch_linear_f32(LinearForm form, const float* a, int64_t lda, const float* b, int64_t ldb, int64_t M, int64_t N,
-                              int64_t K, const EpilogueF32& e, uint32_t* err, int sms, cudaStream_t s);
+                              int64_t K, const EpilogueF32& e, const ColumnSums& cs, uint32_t* err, int sms, cudaStream_t s);
 
 }  // namespace dsv4v

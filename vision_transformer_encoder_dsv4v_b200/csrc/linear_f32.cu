@@ -14,7 +14,7 @@
 // Roles (544 threads): warps 0 to 15 load fp32, split it and write the parts into a 3-stage ring
 // (K-major, 128-byte swizzle, transposing where the contraction is not contiguous), and add up the
 // accumulators, 16 columns each; warp 16 issues the MMAs.  All store the 128 x 64 tile at the end.
-// Loading and splitting bounds it, then the MMAs.  Where there are fewer tiles than SMs, two or four
+// Loading and splitting bounds it, then the MMAs.  Where there are fewer tiles than SMs, two to eight
 // CTAs of a cluster share one, each with a part of the contraction; a rank stores its share of the
 // rows and fetches the others' sums through distributed shared memory, in rank order.
 #include <algorithm>
@@ -36,6 +36,8 @@ constexpr int kStageBytes = 3 * (kABytes + kBBytes);
 constexpr int kSmem = 1024 + kStages * kStageBytes + 256;
 constexpr int kAccCols = 3 * TN;  // a0 b0 | a0 b1 + a1 b0 + a2 b0 | a0 b2 + a1 b1
 constexpr int kSumLd = TN + 1;
+constexpr int kSumRows = TM + 32;  // with the rows that an unrolled read may touch behind the tile
+static_assert(kSumRows * kSumLd * 4 <= kStages * kStageBytes, "the sums have to fit the ring");
 
 // bf16 parts of eight values, 16 bytes each.  A value that is not finite, or that rounds to a bf16
 // infinity, gives parts that are not finite, and so do the outputs that it enters: those are
@@ -134,7 +136,8 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 
 template <bool A_K, bool B_K>
 __global__ void __launch_bounds__(kThreads, 1) k_linear_f32(const float* a, int64_t lda, const float* b, int64_t ldb, int64_t M,
-                                                            int64_t N, int64_t K, const EpilogueF32 e, uint32_t* err, const int ks) {
+                                                            int64_t N, int64_t K, const EpilogueF32 e, const ColumnSums cs, uint32_t* err,
+                                                            const int ks) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
@@ -174,6 +177,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_f32(const float* a, int6
   const int64_t all_stages = (K + TK - 1) / TK, first = all_stages * rank / ks;
   const int stages = static_cast<int>(all_stages * (rank + 1) / ks - first);  // this rank's
   float* sums = reinterpret_cast<float*>(smem);  // [TM][kSumLd], once the ring is done with
+  if (!A_K && cs.out && blockIdx.y == 0 && rank == 0 && threadIdx.x < TM && m0 + threadIdx.x < M) {
+    // the bias gradient of dW's rows, from the strips' sums in order
+    float sum = 0.0f;
+#pragma unroll 8
+    for (int i = 0; i < cs.strips; ++i) sum += cs.sums[i * M + m0 + threadIdx.x];
+    cs.out[m0 + threadIdx.x] = sum;
+  }
   if (warp < kConvert / 32) {
     // ------------------------------------------------------------------ load and split, add up
     Share<TM, A_K> pa(a, lda, m0, M, first * TK, K);
@@ -290,40 +300,53 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_f32(const float* a, int6
   }
   if (ks > 1) cluster_sync();  // every rank's sums are in place
   // A thread stores one column of every eighth row, four at a time: their reads are then in flight
-  // together (element by element, the loop took 4 us of a tile's time).
+  // together.
   const int rows = static_cast<int>(min(int64_t(TM), M - m0)), r1 = rows * (rank + 1) / ks;
   const int lc = static_cast<int>(threadIdx.x) % TN;
   const int64_t col = n0 + lc;
   if (threadIdx.x < kConvert && col < N) {
     const float bias = e.bias ? e.bias[col] : 0.0f;
     constexpr int STEP = kConvert / TN, U = 4;
-    for (int lr = rows * rank / ks + static_cast<int>(threadIdx.x) / TN; lr < r1; lr += STEP * U) {
-      float v[U], res[U];
+    int lr = rows * rank / ks + static_cast<int>(threadIdx.x) / TN;
+    float* y = e.y + (m0 + lr) * e.ld_y + col;
+    const float* res = e.residual ? e.residual + (m0 + lr) * e.ld_residual + col : nullptr;
+    float* z = e.z ? e.z + (m0 + lr) * e.ld_z + col : nullptr;
+    const float* sum = sums + lr * kSumLd + lc;
+    for (; lr < r1; lr += STEP * U, sum += STEP * U * kSumLd) {
+      float v[U], add[U] = {0, 0, 0, 0};
+      if (ks == 1) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int at = min(lr + STEP * u, r1 - 1) * kSumLd + lc;
-        res[u] = e.residual ? e.residual[(m0 + min(lr + STEP * u, r1 - 1)) * e.ld_residual + col] : 0.0f;
-        if (ks == 1) {
-          v[u] = sums[at];
-        } else {
-          v[u] = 0.0f;
-          for (int k = 0; k < ks; ++k)
-            v[u] += __uint_as_float(ld_shared_cluster_u32(mapa_shared(smem_u32(sums + at), static_cast<uint32_t>(k))));
+        for (int u = 0; u < U; ++u) v[u] = sum[STEP * u * kSumLd];  // rows behind the end hold sums too
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = 0.0f;
+        const uint32_t at = smem_u32(sum);
+        for (int k = 0; k < ks; ++k) {
+          const uint32_t peer = mapa_shared(at, static_cast<uint32_t>(k));
+#pragma unroll
+          for (int u = 0; u < U; ++u) v[u] += __uint_as_float(ld_shared_cluster_u32(peer + STEP * u * kSumLd * 4u));
         }
+      }
+      if (res) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (lr + STEP * u < r1) add[u] = res[STEP * u * e.ld_residual];
+        res += STEP * U * e.ld_residual;
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t row = m0 + lr + STEP * u;
         if (lr + STEP * u >= r1) break;
         // An infinity would meet the zeros among the other operand's parts, or a large value have
         // become one: the sum of the plain products says what is true.
-        if (!(fabsf(v[u]) <= 3.4028235e38f)) v[u] = plain_dot<A_K, B_K>(a, lda, b, ldb, row, col, K);
-        float y = v[u] + bias;
-        if (e.z) e.z[row * e.ld_z + col] = y;
-        if (e.act == DSV4V_ACT_GELU) y = 0.5f * y * (1.0f + erff(y * 0.70710678118654752f));
-        else if (e.act == DSV4V_ACT_SILU) y = y / (1.0f + expf(-y));
-        e.y[row * e.ld_y + col] = e.residual ? y + res[u] : y;
+        if (!(fabsf(v[u]) <= 3.4028235e38f)) v[u] = plain_dot<A_K, B_K>(a, lda, b, ldb, m0 + lr + STEP * u, col, K);
+        float out = v[u] + bias;
+        if (z) z[STEP * u * e.ld_z] = out;
+        if (e.act == DSV4V_ACT_GELU) out = 0.5f * out * (1.0f + erff(out * 0.70710678118654752f));
+        else if (e.act == DSV4V_ACT_SILU) out = out / (1.0f + expf(-out));
+        y[STEP * u * e.ld_y] = res ? out + add[u] : out;
       }
+      y += STEP * U * e.ld_y;
+      if (z) z += STEP * U * e.ld_z;
     }
   }
   if (ks > 1) {
@@ -334,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_f32(const float* a, int6
 
 template <bool A_K, bool B_K>
 cudaError_t launch(const float* a, int64_t lda, const float* b, int64_t ldb, int64_t M, int64_t N, int64_t K, const EpilogueF32& e,
-                   uint32_t* err, int sms, cudaStream_t s) {
+                   const ColumnSums& cs, uint32_t* err, int sms, cudaStream_t s) {
   auto kern = k_linear_f32<A_K, B_K>;
   static thread_local uint64_t ready = 0;  // devices on which the shared-memory limit is raised
   int dev = 0;
@@ -344,22 +367,99 @@ cudaError_t launch(const float* a, int64_t lda, const float* b, int64_t ldb, int
     if (dev < 64) ready |= uint64_t(1) << dev;
   }
   const int64_t tm = (M + TM - 1) / TM, tn = (N + TN - 1) / TN, stages = (K + TK - 1) / TK;
-  // The split that leaves no SM a second CTA (33 clusters of four fit 148 SMs), two stages a rank at
-  // least.
-  const int ks = tm * tn * 4 <= sms * 132 / 148 && stages >= 8 ? 4 : (tm * tn * 2 <= sms && stages >= 4 ? 2 : 1);
+  // The split that leaves no SM a second CTA (15 clusters of eight and 33 of four fit 148 SMs), two
+  // stages a rank at least.
+  const int64_t tiles = tm * tn;
+  const int ks = tiles <= sms * 15 / 148 && stages >= 16 ? 8
+                 : tiles <= sms * 33 / 148 && stages >= 8 ? 4
+                 : tiles * 2 <= sms && stages >= 4        ? 2
+                                                          : 1;
   const dim3 grid(static_cast<unsigned>(tm * ks), static_cast<unsigned>(tn));
-  if (ks == 1) return launch_pdl(kern, grid, dim3(kThreads), kSmem, s, a, lda, b, ldb, M, N, K, e, err, 1);
-  return launch_pdl_cluster(kern, grid, dim3(kThreads), kSmem, s, static_cast<unsigned>(ks), a, lda, b, ldb, M, N, K, e, err, ks);
+  if (ks == 1) return launch_pdl(kern, grid, dim3(kThreads), kSmem, s, a, lda, b, ldb, M, N, K, e, cs, err, 1);
+  return launch_pdl_cluster(kern, grid, dim3(kThreads), kSmem, s, static_cast<unsigned>(ks), a, lda, b, ldb, M, N, K, e, cs, err, ks);
+}
+
+// ---------------------------------------------------------------------------- a few rows
+// y of one to four rows: a warp streams the weights of an output feature at a time against the rows
+// of x in shared memory, as k_linear_few does for bf16 (1 x 1024 x 1024: 3 us, where a 128-row tile
+// takes 12 us).
+constexpr int kFewThreads = 256, kFewSmem = 48 * 1024;
+
+template <int R>
+__global__ void __launch_bounds__(kFewThreads) k_linear_few_f32(const float* x, int64_t ld_x, const float* w, int64_t ld_w, int rows,
+                                                                int N, int K, bool vec, const EpilogueF32 e) {
+  extern __shared__ float sx[];  // [R][K rounded up to 4]
+  const int lane = threadIdx.x & 31, ld_s = (K + 3) / 4 * 4;
+  launch_dependents();
+  grid_dependency_wait();
+  for (int i = threadIdx.x; i < R * ld_s; i += kFewThreads) {
+    const int r = i / ld_s, k = i - r * ld_s;
+    sx[i] = r < rows && k < K ? x[r * ld_x + k] : 0.0f;
+  }
+  __syncthreads();
+  const int warps = static_cast<int>(gridDim.x) * (kFewThreads / 32);
+  for (int f = static_cast<int>(blockIdx.x) * (kFewThreads / 32) + (threadIdx.x >> 5); f < N; f += warps) {
+    const float* wf = w + static_cast<int64_t>(f) * ld_w;
+    float acc[R] = {};
+    int k = 0;
+    if (vec) {
+#pragma unroll 4
+      for (; k + 128 <= K; k += 128) {
+        const float4 q = *reinterpret_cast<const float4*>(wf + k + 4 * lane);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float4 v = *reinterpret_cast<const float4*>(sx + r * ld_s + k + 4 * lane);
+          acc[r] = fmaf(q.x, v.x, fmaf(q.y, v.y, fmaf(q.z, v.z, fmaf(q.w, v.w, acc[r]))));
+        }
+      }
+    }
+#pragma unroll 4
+    for (int i = k + lane; i < K; i += 32) {
+      const float q = wf[i];
+#pragma unroll
+      for (int r = 0; r < R; ++r) acc[r] = fmaf(q, sx[r * ld_s + i], acc[r]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int r = 0; r < R; ++r) acc[r] += __shfl_xor_sync(0xffffffffu, acc[r], o);
+    float v = acc[0];
+#pragma unroll
+    for (int r = 1; r < R; ++r)
+      if (lane == r) v = acc[r];
+    if (lane < rows) {  // lane r finishes row r
+      if (e.bias) v += e.bias[f];
+      if (e.z) e.z[lane * e.ld_z + f] = v;
+      if (e.act == DSV4V_ACT_GELU) v = 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+      else if (e.act == DSV4V_ACT_SILU) v = v / (1.0f + expf(-v));
+      if (e.residual) v += e.residual[lane * e.ld_residual + f];
+      e.y[lane * e.ld_y + f] = v;
+    }
+  }
+}
+
+template <int R>
+cudaError_t launch_few(const float* x, int64_t ld_x, const float* w, int64_t ld_w, int64_t rows, int64_t N, int64_t K,
+                       const EpilogueF32& e, int sms, cudaStream_t s) {
+  const int64_t per = kFewThreads / 32;
+  const int grid = static_cast<int>(std::min<int64_t>((N + per - 1) / per, sms * 4));
+  const bool vec = (reinterpret_cast<uintptr_t>(w) & 15) == 0 && ld_w % 4 == 0;
+  return launch_pdl(k_linear_few_f32<R>, dim3(grid), dim3(kFewThreads), static_cast<size_t>(R) * ((K + 3) / 4 * 16), s, x, ld_x, w, ld_w,
+                    static_cast<int>(rows), static_cast<int>(N), static_cast<int>(K), vec, e);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_f32(LinearForm form, const float* a, int64_t lda, const float* b, int64_t ldb, int64_t M, int64_t N,
-                              int64_t K, const EpilogueF32& e, uint32_t* err, int sms, cudaStream_t s) {
+                              int64_t K, const EpilogueF32& e, const ColumnSums& cs, uint32_t* err, int sms, cudaStream_t s) {
+  if (form == LINEAR_FORWARD && M <= 4 && (M <= 2 ? M : 4) * ((K + 3) / 4 * 16) <= kFewSmem)
+    return M == 1   ? launch_few<1>(a, lda, b, ldb, M, N, K, e, sms, s)
+           : M == 2 ? launch_few<2>(a, lda, b, ldb, M, N, K, e, sms, s)
+                    : launch_few<4>(a, lda, b, ldb, M, N, K, e, sms, s);
   switch (form) {
-    case LINEAR_FORWARD: return launch<true, true>(a, lda, b, ldb, M, N, K, e, err, sms, s);
-    case LINEAR_INPUT_GRAD: return launch<true, false>(a, lda, b, ldb, M, N, K, e, err, sms, s);
-    case LINEAR_WEIGHT_GRAD: return launch<false, false>(a, lda, b, ldb, M, N, K, e, err, sms, s);
+    case LINEAR_FORWARD: return launch<true, true>(a, lda, b, ldb, M, N, K, e, cs, err, sms, s);
+    case LINEAR_INPUT_GRAD: return launch<true, false>(a, lda, b, ldb, M, N, K, e, cs, err, sms, s);
+    case LINEAR_WEIGHT_GRAD: return launch<false, false>(a, lda, b, ldb, M, N, K, e, cs, err, sms, s);
   }
   return cudaErrorInvalidValue;
 }
