@@ -271,12 +271,13 @@ def test_linear_fp32_values_that_bf16_cannot_hold():
     x[8, 1], x[9, 2], x[10, 4] = float("inf"), float("nan"), -float("inf")
     w[20, 1] = 0.0                          # infinity times zero
     x[11], x[12] = 1e-30, 1e30
-    want = np64(x) @ np64(w).T
+    with np.errstate(invalid="ignore"):
+        want = np64(x) @ np64(w).T
     y = torch.empty(rows, n, device="cuda")
     A.dsv4v_linear_forward(A.make_linear(rows, k, n, dtype=A.DSV4V_F32), x, w, None, None, None, y)
     got = np64(y)
-    over = np.abs(want) > big
-    want = np.where(over & np.isfinite(want), np.sign(want) * np.inf, want)
+    over = np.isfinite(want) & (np.abs(want) > big)
+    want[over] = np.sign(want[over]) * np.inf
     assert np.array_equal(np.isnan(got), np.isnan(want))
     assert np.array_equal(got[np.isinf(want)], want[np.isinf(want)])
     ok = np.isfinite(want)
@@ -363,3 +364,65 @@ def test_linear_on_another_stream_and_two_at_once():
         torch.cuda.synchronize()
         for a, b in zip(want, got):
             assert all(torch.equal(p, q) for p, q in zip(a[:5], b[:5]))
+
+
+def test_linear_beyond_32_bit_offsets():
+    # outputs of over 2^31 elements: the last rows are those of a layer of their own
+    rows, k, n, last = 70001, 16, 32776, 300
+    x, w = normal((rows, k), 1.0, torch.bfloat16, 1), normal((n, k), 0.25, torch.bfloat16, 2)
+    y = torch.empty(rows, n, dtype=torch.bfloat16, device="cuda")
+    A.dsv4v_linear_forward(A.make_linear(rows, k, n, A.ACT_SILU), x, w, None, None, None, y)
+    want = O.forward(np64(x[-last:]), np64(w), act="silu")[0]
+    assert np.linalg.norm(np64(y[-last:]) - want) <= 2.0 ** -8 * np.linalg.norm(want)
+    layer = A.make_linear(rows, k, n)
+    ws = torch.empty(A.dsv4v_linear_backward_workspace_size(layer), dtype=torch.uint8, device="cuda")
+    dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty(n, device="cuda")
+    y[:-last] = 0  # d_y: only the last rows count
+    A.dsv4v_linear_backward(layer, x, w, None, y, dx, dw, db, ws)
+    dy = np64(y[-last:])
+    want_dx, want_dw, want_db, _ = O.backward(np64(x[-last:]), np64(w), None, dy)
+    for got, want in ((dx[-last:], want_dx), (dw, want_dw)):
+        assert np.linalg.norm(np64(got) - want) <= 2.0 ** -8 * np.linalg.norm(want)
+    assert np.abs(np64(db) - want_db).max() <= (last + 16) * 2.0 ** -24 * np.abs(dy).sum(0).max()
+    assert not dx[:-last].any() and A.dsv4v_device_error() == 0
+
+
+FIRST_CALL = """
+import torch
+from vision_transformer_encoder_dsv4v_b200 import dsv4v as A
+x, w = torch.randn(300, 256, device="cuda").bfloat16(), torch.randn(304, 256, device="cuda").bfloat16()
+y, z = torch.empty(300, 304, device="cuda").bfloat16(), torch.empty(300, 304, device="cuda").bfloat16()
+dx, dw, db, norm = torch.empty_like(x), torch.empty_like(w), torch.empty(304, device="cuda"), torch.empty((), device="cuda")
+m, v = torch.zeros(w.numel(), device="cuda"), torch.zeros(w.numel(), device="cuda")
+layer = A.make_linear(300, 256, 304, A.ACT_GELU)
+ws = torch.empty(A.dsv4v_linear_backward_workspace_size(layer), dtype=torch.uint8, device="cuda")
+grads, table = A.GradTable([dw, db]), A.AdamwTable([dict(param=w, grad=dw, exp_avg=m, exp_avg_sq=v)])
+nws = torch.empty(A.dsv4v_grad_norm_workspace_size(grads), dtype=torch.uint8, device="cuda")
+def step():
+    A.dsv4v_linear_forward(layer, x, w, None, None, z, y)
+    A.dsv4v_linear_backward(layer, x, w, z, y, dx, dw, db, ws)
+    A.dsv4v_grad_norm(grads, norm, nws)
+    A.dsv4v_adamw_step(A.make_adamw(1e-3), table, grad_norm=norm)
+w0 = w.clone()
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    step()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in (y, dx, dw, db, norm, w)]
+w.copy_(w0), m.zero_(), v.zero_()
+step()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, (y, dx, dw, db, norm, w))) and not torch.equal(w, w0)
+print("first call captured")
+"""
+
+
+def test_a_programs_first_calls_may_be_captured():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], capture_output=True, text=True, cwd=root, timeout=240)
+    assert r.returncode == 0 and "first call captured" in r.stdout, r.stderr[-2000:]

@@ -812,7 +812,11 @@ dsv4v_status prepare_rows(const dsv4v_config* cfg, int64_t rows, void* workspace
 
 bool query_device(int* sms, uint32_t** err) {
   DeviceInfo info;
-  if (!device_info(info)) return false;
+  try {
+    if (!device_info(info)) return false;
+  } catch (...) {  // the cache could not grow
+    return false;
+  }
   if (sms) *sms = info.sms;
   if (err) *err = info.err;
   return true;
