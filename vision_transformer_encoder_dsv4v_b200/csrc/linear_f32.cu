@@ -40,8 +40,8 @@ constexpr int kSumRows = TM + 32;  // with the rows that an unrolled read may to
 static_assert(kSumRows * kSumLd * 4 <= kStages * kStageBytes, "the sums have to fit the ring");
 
 // bf16 parts of eight values, 16 bytes each.  A value that is not finite, or that rounds to a bf16
-// infinity, gives parts that are not finite, and so do the outputs that it enters: those are
-// computed again in fp32 (see the end of the kernel).
+// infinity, gives parts that are not finite, and so are the sums that it enters: their tiles are
+// computed again in fp32 (see store_column_plain).
 __device__ __forceinline__ void split8(const float (&x)[8], uint4 (&out)[3]) {
   uint32_t w[3][4];
 #pragma unroll
@@ -56,20 +56,6 @@ __device__ __forceinline__ void split8(const float (&x)[8], uint4 (&out)[3]) {
   }
 #pragma unroll
   for (int q = 0; q < 3; ++q) out[q] = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
-}
-
-// Row r of A times row c of B, in fp32.
-template <bool A_K, bool B_K>
-__device__ __noinline__ float plain_dot(const float* a, int64_t lda, const float* b, int64_t ldb, int64_t r, int64_t c, int64_t K) {
-  const float* pa = A_K ? a + r * lda : a + r;
-  const float* pb = B_K ? b + c * ldb : b + c;
-  float sum = 0.0f;
-  for (int64_t k0 = 0; k0 < K; k0 += 128) {
-    float part = 0.0f;
-    for (int64_t k = k0; k < min(K, k0 + 128); ++k) part = fmaf(pa[A_K ? k : k * lda], pb[B_K ? k : k * ldb], part);
-    sum += part;
-  }
-  return sum;
 }
 
 // A thread's share of an operand's ROWS x 64 part of a stage, in pieces of one row and eight
@@ -130,6 +116,81 @@ struct Share {
   }
 };
 
+// ---------------------------------------------------------------------------- epilogue
+__device__ __forceinline__ float activate(float v, int act) {
+  if (act == DSV4V_ACT_GELU) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+  return act == DSV4V_ACT_SILU ? v / (1.0f + expf(-v)) : v;
+}
+
+// Stores rows lr, lr + 8, .. below r1 of one column of a tile: y, z and res point at row lr, `sum` at
+// its sum (KS ranks: in every rank's shared memory).  Four rows at a time, whose reads are then in
+// flight together.
+template <int KS>
+__device__ __forceinline__ void store_column(const EpilogueF32& e, int lr, int r1, const float* sum, float bias, float* y,
+                                             const float* res, float* z) {
+  constexpr int STEP = kConvert / TN, U = 4;
+  for (; lr < r1; lr += STEP * U, sum += STEP * U * kSumLd) {
+    float v[U], add[U] = {0, 0, 0, 0};
+    if constexpr (KS == 1) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = sum[STEP * u * kSumLd];  // rows behind the end hold sums too
+    } else {
+      float q[KS][U];
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const uint32_t peer = mapa_shared(smem_u32(sum), static_cast<uint32_t>(k));
+#pragma unroll
+        for (int u = 0; u < U; ++u) q[k][u] = __uint_as_float(ld_shared_cluster_u32(peer + STEP * u * kSumLd * 4u));
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        v[u] = q[0][u];
+#pragma unroll
+        for (int k = 1; k < KS; ++k) v[u] += q[k][u];
+      }
+    }
+    if (res) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (lr + STEP * u < r1) add[u] = res[STEP * u * e.ld_residual];
+      res += STEP * U * e.ld_residual;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (lr + STEP * u >= r1) break;
+      const float pre = v[u] + bias;
+      if (z) z[STEP * u * e.ld_z] = pre;
+      const float out = activate(pre, e.act);
+      y[STEP * u * e.ld_y] = res ? out + add[u] : out;
+    }
+    y += STEP * U * e.ld_y;
+    if (z) z += STEP * U * e.ld_z;
+  }
+}
+
+// The same from plain fp32 products of the operands, for a tile with values that are not finite or
+// near the end of fp32's range: an infinity meets the zeros among the other operand's parts, and a
+// large value may have rounded to one, where the plain products say what is true.
+template <bool A_K, bool B_K>
+__device__ __noinline__ void store_column_plain(const EpilogueF32& e, const float* a, int64_t lda, const float* b, int64_t ldb, int64_t K,
+                                                int64_t row, int64_t row_end, int64_t col) {
+  const float* pb = B_K ? b + col * ldb : b + col;
+  for (; row < row_end; row += kConvert / TN) {
+    const float* pa = A_K ? a + row * lda : a + row;
+    float v = 0.0f;
+    for (int64_t k0 = 0; k0 < K; k0 += 128) {
+      float part = 0.0f;
+      for (int64_t k = k0; k < min(K, k0 + 128); ++k) part = fmaf(pa[A_K ? k : k * lda], pb[B_K ? k : k * ldb], part);
+      v += part;
+    }
+    if (e.bias) v += e.bias[col];
+    if (e.z) e.z[row * e.ld_z + col] = v;
+    v = activate(v, e.act);
+    if (e.residual) v += e.residual[row * e.ld_residual + col];
+    e.y[row * e.ld_y + col] = v;
+  }
+}
+
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* err, uint32_t code) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err, code));
 }
@@ -147,6 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_f32(const float* a, int6
   uint64_t* mma_done = cempty + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  volatile int* wild = abort_flag + 1;  // a sum that is not finite, or large
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -159,6 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_f32(const float* a, int6
     }
     mbar_init(mma_done, 1);
     *abort_flag = 0;
+    *wild = 0;
     fence_mbar_init();
   }
   if (warp == kConvert / 32) {
@@ -251,8 +314,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_f32(const float* a, int6
     while (ok && chunk < chunks) add_up();
     // The last accumulator is complete, so every MMA has read the ring.
     if (ok) {
+      bool fine = true;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) sums[(quad * 32 + lane) * kSumLd + col + j] = v[j];
+      for (int j = 0; j < 16; ++j) {
+        sums[(quad * 32 + lane) * kSumLd + col + j] = v[j];
+        fine = fine && fabsf(v[j]) <= 1e37f;  // eight of these stay below the end of fp32's range
+      }
+      if (!fine && m0 + quad * 32 + lane < M) *wild = 1;
     }
   } else {
     // ------------------------------------------------------------------ MMAs
@@ -299,55 +367,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_f32(const float* a, int6
     tmem_dealloc(tmem, 512);
   }
   if (ks > 1) cluster_sync();  // every rank's sums are in place
-  // A thread stores one column of every eighth row, four at a time: their reads are then in flight
-  // together.
+  // A thread stores one column of every eighth row.
   const int rows = static_cast<int>(min(int64_t(TM), M - m0)), r1 = rows * (rank + 1) / ks;
-  const int lc = static_cast<int>(threadIdx.x) % TN;
-  const int64_t col = n0 + lc;
+  const int lc = static_cast<int>(threadIdx.x) % TN, lr = rows * rank / ks + static_cast<int>(threadIdx.x) / TN;
+  const int64_t row = m0 + lr, col = n0 + lc;
+  bool large = *wild;
+  for (int k = 0; k < ks && ks > 1; ++k)
+    large |= ld_shared_cluster_u32(mapa_shared(smem_u32(const_cast<int*>(wild)), static_cast<uint32_t>(k))) != 0;
   if (threadIdx.x < kConvert && col < N) {
     const float bias = e.bias ? e.bias[col] : 0.0f;
-    constexpr int STEP = kConvert / TN, U = 4;
-    int lr = rows * rank / ks + static_cast<int>(threadIdx.x) / TN;
-    float* y = e.y + (m0 + lr) * e.ld_y + col;
-    const float* res = e.residual ? e.residual + (m0 + lr) * e.ld_residual + col : nullptr;
-    float* z = e.z ? e.z + (m0 + lr) * e.ld_z + col : nullptr;
     const float* sum = sums + lr * kSumLd + lc;
-    for (; lr < r1; lr += STEP * U, sum += STEP * U * kSumLd) {
-      float v[U], add[U] = {0, 0, 0, 0};
-      if (ks == 1) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) v[u] = sum[STEP * u * kSumLd];  // rows behind the end hold sums too
-      } else {
-#pragma unroll
-        for (int u = 0; u < U; ++u) v[u] = 0.0f;
-        const uint32_t at = smem_u32(sum);
-        for (int k = 0; k < ks; ++k) {
-          const uint32_t peer = mapa_shared(at, static_cast<uint32_t>(k));
-#pragma unroll
-          for (int u = 0; u < U; ++u) v[u] += __uint_as_float(ld_shared_cluster_u32(peer + STEP * u * kSumLd * 4u));
-        }
-      }
-      if (res) {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (lr + STEP * u < r1) add[u] = res[STEP * u * e.ld_residual];
-        res += STEP * U * e.ld_residual;
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (lr + STEP * u >= r1) break;
-        // An infinity would meet the zeros among the other operand's parts, or a large value have
-        // become one: the sum of the plain products says what is true.
-        if (!(fabsf(v[u]) <= 3.4028235e38f)) v[u] = plain_dot<A_K, B_K>(a, lda, b, ldb, m0 + lr + STEP * u, col, K);
-        float out = v[u] + bias;
-        if (z) z[STEP * u * e.ld_z] = out;
-        if (e.act == DSV4V_ACT_GELU) out = 0.5f * out * (1.0f + erff(out * 0.70710678118654752f));
-        else if (e.act == DSV4V_ACT_SILU) out = out / (1.0f + expf(-out));
-        y[STEP * u * e.ld_y] = res ? out + add[u] : out;
-      }
-      y += STEP * U * e.ld_y;
-      if (z) z += STEP * U * e.ld_z;
-    }
+    float* y = e.y + row * e.ld_y + col;
+    const float* res = e.residual ? e.residual + row * e.ld_residual + col : nullptr;
+    float* z = e.z ? e.z + row * e.ld_z + col : nullptr;
+    if (large) store_column_plain<A_K, B_K>(e, a, lda, b, ldb, K, row, m0 + r1, col);
+    else if (ks == 1) store_column<1>(e, lr, r1, sum, bias, y, res, z);
+    else if (ks == 2) store_column<2>(e, lr, r1, sum, bias, y, res, z);
+    else if (ks == 4) store_column<4>(e, lr, r1, sum, bias, y, res, z);
+    else store_column<8>(e, lr, r1, sum, bias, y, res, z);
   }
   if (ks > 1) {
     __syncwarp();
