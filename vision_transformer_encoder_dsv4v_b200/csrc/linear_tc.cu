@@ -734,7 +734,7 @@ constexpr int kFewSmem = 48 * 1024;
 
 // F features a warp share what it reads of x.
 template <int R, int F>
-__global__ void __launch_bounds__(kFewThreads, 4) k_linear_few(const __nv_bfloat16* x, int64_t ld_x, const __nv_bfloat16* w,
+__global__ void __launch_bounds__(kFewThreads, F == 1 ? 4 : 2) k_linear_few(const __nv_bfloat16* x, int64_t ld_x, const __nv_bfloat16* w,
                                                             int64_t ld_w, int rows, int N, int K, const LinearEpilogue e) {
   // x in fp32, R rows of k8 pieces of 8; a piece's halves lie in two planes, so that the 16-byte
   // reads of a warp are contiguous
@@ -856,7 +856,7 @@ cudaError_t launch_few(const void* x, int64_t ld_x, const void* w, int64_t ld_w,
 }  // namespace
 
 // Up to four rows, as long as they fit shared memory and the sharing of x does not cost more than
-// the tensor-core kernel's set-up (1 x 4608 x 4608: 9.5 us against 12.0 us; 2 rows 11.5 against 12.4;
+// the tensor-core kernel's set-up (1 x 4608 x 4608: 9.5 us against 12.0 us; 2 rows 10.6 against 12.2;
 // 4 rows of 1024 x 2816 4.1 against 5.0, of 2816 x 1024 5.9 against 5.3).
 bool linear_is_few(int64_t M, int64_t K) { return M <= 2 ? M * K * 4 <= kFewSmem : (M <= 4 && K <= 2048); }
 
