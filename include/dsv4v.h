@@ -517,7 +517,9 @@ typedef struct {
  *   z: device [rows, out_features], written for dsv4v_linear_backward, or NULL.
  *   y: device [rows, out_features], written.  Elements between a row's end and the next row are
  *   left as they were.
- * Needs no workspace; the result does not depend on the schedule. */
+ * Needs no workspace; the result does not depend on the schedule.  Unlike the calls above, this one
+ * and dsv4v_linear_backward read nothing, w included, before the kernels ahead of them on the stream
+ * have finished: w may be another call's output. */
 dsv4v_status dsv4v_linear_forward(const dsv4v_linear* layer, const void* x, const void* w, const float* bias,
                                   const void* residual, void* z, void* y, void* stream);
 
