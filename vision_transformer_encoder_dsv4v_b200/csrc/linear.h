@@ -35,16 +35,29 @@ enum LinearForm {
   LINEAR_FORWARD,      // D[rows, out] = x . W^T: both operands K-major
   LINEAR_INPUT_GRAD,   // dx[rows, in] = dz . W: dz K-major, W MN-major
   LINEAR_WEIGHT_GRAD,  // dW[out, in] = dz^T . x: both MN-major
+  LINEAR_BOTH_GRADS,   // dx and dW in one launch
 };
 
+// How a launch is cut up; the second entries are dW's of LINEAR_BOTH_GRADS.
 struct LinearPlan {
   int pair = 0, bn = 0, ks = 1;  // CTA pairs; columns of a tile; K splits (cluster size)
-  int tiles_m = 0, tiles_n = 0, kb_total = 0 /* stages */, grid = 0;
+  int tiles_m[2] = {}, tiles_n[2] = {}, kb_total[2] = {} /* stages */, grid = 0;
+  int units = 0;                 // of LINEAR_BOTH_GRADS: CTAs (pairs) of dx
   int a_rows = 0;                // rows of the boxes of a K-major A
+  double us = 0;                 // estimated time
+};
+struct LinearMaps {
+  CUtensorMap a[2], b[2];
+};
+struct LinearProduct {
+  int M, N;
+  LinearEpilogue e;
 };
 
 // Tile, pairing and split of D[M, N] over a contraction of K, on `sms` SMs.
 LinearPlan plan_linear(LinearForm form, int64_t M, int64_t N, int64_t K, int sms);
+// The same for both gradients of a layer in one launch.
+LinearPlan plan_linear_both(int64_t rows, int64_t in, int64_t out, int sms);
 // Depth of a stage, and rows of the boxes of A's and B's tensor maps (for an MN-major operand, rows
 // of the contraction) under a plan.
 inline int linear_depth(const LinearPlan& p) { return p.bn <= 192 ? 128 : 64; }
@@ -56,8 +69,8 @@ bool linear_is_few(int64_t M, int64_t K);
 cudaError_t launch_linear_few(const void* x, int64_t ld_x, const void* w, int64_t ld_w, int M, int N, int K, const LinearEpilogue& e,
                               int sms, cudaStream_t s);
 
-cudaError_t launch_linear(LinearForm form, const LinearPlan& plan, const CUtensorMap& ta, const CUtensorMap& tb, int M, int N,
-                          const LinearEpilogue& e, const ColumnSums& cs, uint32_t* err, cudaStream_t s);
+cudaError_t launch_linear(LinearForm form, const LinearPlan& plan, const LinearMaps& maps, const LinearProduct* products,
+                          const ColumnSums& cs, uint32_t* err, cudaStream_t s);
 
 // The same for fp32 matrices (linear_f32.cu).
 struct EpilogueF32 {

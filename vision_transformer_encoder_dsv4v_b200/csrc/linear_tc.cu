@@ -158,22 +158,28 @@ __device__ __forceinline__ void commit_to(uint32_t bar) {
     asm volatile(ELECTED("@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t") ::"r"(bar) : "memory");
 }
 
-struct Params {
+// One product of a launch.
+struct Job {
   int M, N;              // extents of D
   int tiles_m, tiles_n;  // BM (PAIR: 2 BM) x BN tiles
   int kb_total;          // stages of the contraction, 64 KPS deep
-  int a_rows;            // rows of a K-major A's boxes: fewer than BM where D has fewer (the MMA then
-                         // reads what lies behind them, into accumulator rows that nobody looks at)
-  int stages;            // of the ring
   LinearEpilogue e;
-  ColumnSums cs;         // weight gradient: the bias gradient that goes with it
+};
+
+struct Params {
+  Job job[2];    // both gradients in one launch: the input's, the weight's
+  int units;     // CTAs (PAIR: pairs) that take the first of two jobs
+  int a_rows;    // rows of a K-major A's boxes: fewer than BM where D has fewer (the MMA then reads
+                 // what lies behind them, into accumulator rows that nobody looks at)
+  int stages;    // of the ring
+  ColumnSums cs; // weight gradient: the bias gradient that goes with it
   uint32_t* err;
 };
 
 // Tile t in an order that keeps the tiles in flight together compact (kGroupM row tiles by as many
 // column tiles as it takes), so that they share their operands in L2: with whole columns of 64 row
 // tiles a wave of the 16384 x 4096 x 4608 product would fetch 155 MB, with groups 40 MB.
-__device__ __forceinline__ void tile_at(const Params& p, int t, int& m, int& n) {
+__device__ __forceinline__ void tile_at(const Job& p, int t, int& m, int& n) {
   const int per = kGroupM * p.tiles_n, g = t / per, r = t - g * per;
   const int rows = min(kGroupM, p.tiles_m - g * kGroupM);
   n = r / rows;
@@ -268,19 +274,19 @@ __device__ __forceinline__ uint4 pack8(const float* v) {
 
 // The bias gradient of rows m0 .. m0 + 127 of dW: the strips' sums, in order.  The epilogue warps have
 // the time of a tile's main loop for it.
-__device__ __forceinline__ void sum_columns(const Params& p, int m0) {
+__device__ __forceinline__ void sum_columns(const ColumnSums& cs, int M, int m0) {
   const int t = static_cast<int>(threadIdx.x) - 64, f = m0 + t;
-  if (t >= BM || f >= p.M) return;
+  if (t >= BM || f >= M) return;
   float sum = 0.0f;
 #pragma unroll 8
-  for (int i = 0; i < p.cs.strips; ++i) sum += p.cs.sums[static_cast<int64_t>(i) * p.M + f];
-  p.cs.out[f] = sum;
+  for (int i = 0; i < cs.strips; ++i) sum += cs.sums[static_cast<int64_t>(i) * M + f];
+  cs.out[f] = sum;
 }
 
 // Cluster split-K: this rank's share of a tile.  The tile's 8-column pieces are dealt to the ranks
 // in turn; a piece's partials are all fetched, then summed in rank order.
 template <int BN, bool FWD, int KS>
-__device__ __forceinline__ void finish_pieces(const Params& p, float* part, int slice, int rows, int m0, int n0) {
+__device__ __forceinline__ void finish_pieces(const Job& p, float* part, int slice, int rows, int m0, int n0) {
   constexpr int PIECES = BN / 8, LD = Tile<BN, false>::PART_LD;
   const LinearEpilogue& e = p.e;
   uint32_t base[KS];
@@ -342,20 +348,29 @@ __device__ __forceinline__ void finish_pieces(const Params& p, float* part, int 
 }
 
 // ---------------------------------------------------------------------------- kernel
-// A_MN / B_MN: the operand is MN-major, loaded as 64 x 64 boxes of its stored [K, MN] matrix (atom
-// columns of 8 KB); else K-major, one box of 64 columns.  FWD: bias, activation, residual and the
-// saved pre-activation; without it D is stored as it is.  KS (cluster split-K) is the cluster's
-// size, 1 to 8.
-template <int BN, bool PAIR, bool A_MN, bool B_MN, bool FWD>
+// An MN-major operand is loaded as boxes of 64 columns of its stored [K, MN] matrix (atom columns of
+// 64 KPS rows); else K-major, in boxes of 64 columns of its rows.  The forward has bias, activation,
+// residual and the saved pre-activation; the gradients store D as it is.  LINEAR_BOTH_GRADS splits
+// the CTAs between the two gradients.  KS (cluster split-K) is the cluster's size, 1 to 8.
+template <int BN, bool PAIR, LinearForm FORM>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_linear(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+    k_linear(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ CUtensorMap tm_b0,
+             const __grid_constant__ CUtensorMap tm_a1, const __grid_constant__ CUtensorMap tm_b1,
              const __grid_constant__ Params p, const int ks) {
+  constexpr bool BOTH = FORM == LINEAR_BOTH_GRADS, FWD = FORM == LINEAR_FORWARD, B_MN = !FWD;
   using T = Tile<BN, PAIR>;
   constexpr int KPS = T::KPS;
   constexpr int BMT = PAIR ? 2 * BM : BM;
+  const int span = PAIR ? 2 : ks;  // CTAs that share a tile
+  const int unit = static_cast<int>(blockIdx.x) / span, units = static_cast<int>(gridDim.x) / span;
+  const bool second = BOTH && unit >= p.units;
+  const Job& job = p.job[second ? 1 : 0];
+  const bool a_mn = BOTH ? second : FORM == LINEAR_WEIGHT_GRAD;
+  const CUtensorMap* tm_a = second ? &tm_a1 : &tm_a0;
+  const CUtensorMap* tm_b = second ? &tm_b1 : &tm_b0;
   // One step's A and B; a stage is KPS A's, then KPS B's.  An MN-major operand's atom columns hold
   // the stage's whole depth.
-  const uint32_t a_bytes = A_MN ? BM * BK * 2 : static_cast<uint32_t>(p.a_rows) * BK * 2;
+  const uint32_t a_bytes = FORM == LINEAR_WEIGHT_GRAD ? BM * BK * 2 : static_cast<uint32_t>(p.a_rows) * BK * 2;
   const uint32_t stage_bytes = KPS * (a_bytes + T::B_BYTES);
   constexpr uint32_t kAtom = 8192 * KPS;
   extern __shared__ uint8_t smem_raw[];
@@ -373,11 +388,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t rank = PAIR ? crank : 0u;  // 0: the pair's leader, which issues the MMAs
   // This CTA's share of the contraction, and the tiles it takes.
   const int slice = ks > 1 ? static_cast<int>(crank) : 0;
-  const int kb0 = static_cast<int>(static_cast<int64_t>(slice) * p.kb_total / ks);
-  const int kb1 = static_cast<int>(static_cast<int64_t>(slice + 1) * p.kb_total / ks);
-  const int span = PAIR ? 2 : ks;  // CTAs that share a tile
-  const int t_first = static_cast<int>(blockIdx.x) / span, t_step = static_cast<int>(gridDim.x) / span;
-  const int tiles = p.tiles_m * p.tiles_n;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(slice) * job.kb_total / ks);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(slice + 1) * job.kb_total / ks);
+  const int t_first = second ? unit - p.units : unit, t_step = BOTH ? (second ? units - p.units : p.units) : units;
+  const int tiles = job.tiles_m * job.tiles_n;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
@@ -391,8 +405,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&tm_a);
-    tma_prefetch_desc(&tm_b);
+    tma_prefetch_desc(tm_a);
+    tma_prefetch_desc(tm_b);
   }
   if (warp == 1) {
     if constexpr (PAIR) {
@@ -433,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tx = (PAIR ? 2 : 1) * stage_bytes;
     for (int t = t_first; t < tiles; t += t_step) {
       int mt, nt;
-      tile_at(p, t, mt, nt);
+      tile_at(job, t, mt, nt);
       const int m0 = mt * BMT + static_cast<int>(rank) * BM;
       const int n0 = nt * BN + static_cast<int>(rank) * (BN / 2) * (PAIR ? 1 : 0);
       for (int kb = kb0; kb < kb1; ++kb) {
@@ -442,19 +456,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t sa = ring + static_cast<uint32_t>(stage) * stage_bytes, sb = sa + KPS * a_bytes, bar = full_leader + 8u * stage;
           if (posts) bar_expect(full_bar + 8u * stage, tx);
           const int k0 = kb * (KPS * BK);
-          if constexpr (A_MN) {
+          if (a_mn) {
 #pragma unroll
-            for (int j = 0; j < BM / 64; ++j) tma_tile<PAIR>(sa + j * kAtom, &tm_a, bar, m0 + 64 * j, k0);
+            for (int j = 0; j < BM / 64; ++j) tma_tile<PAIR>(sa + j * kAtom, tm_a, bar, m0 + 64 * j, k0);
           } else {
 #pragma unroll
-            for (int j = 0; j < KPS; ++j) tma_tile<PAIR>(sa + j * a_bytes, &tm_a, bar, k0 + j * BK, m0);
+            for (int j = 0; j < KPS; ++j) tma_tile<PAIR>(sa + j * a_bytes, tm_a, bar, k0 + j * BK, m0);
           }
           if constexpr (B_MN) {
 #pragma unroll
-            for (int j = 0; j < T::B_ROWS / 64; ++j) tma_tile<PAIR>(sb + j * kAtom, &tm_b, bar, n0 + 64 * j, k0);
+            for (int j = 0; j < T::B_ROWS / 64; ++j) tma_tile<PAIR>(sb + j * kAtom, tm_b, bar, n0 + 64 * j, k0);
           } else {
 #pragma unroll
-            for (int j = 0; j < KPS; ++j) tma_tile<PAIR>(sb + j * T::B_BYTES, &tm_b, bar, k0 + j * BK, n0);
+            for (int j = 0; j < KPS; ++j) tma_tile<PAIR>(sb + j * T::B_BYTES, tm_b, bar, k0 + j * BK, n0);
           }
           issued |= 1u << stage;
           issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
@@ -482,10 +496,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       volatile int never = 0;  // its TMEM is written until the leader's final commit
       mbar_wait(mma_done, 0, &never, p.err, kErrTimeoutMma);
     } else {
-      constexpr uint32_t idesc = idesc_bf16_mn(BMT, BN, A_MN, B_MN);
-      constexpr uint64_t kStepA = A_MN ? 128 : 2, kStepB = B_MN ? 128 : 2;  // 16 of K, in 16-byte units
+      const uint32_t idesc = a_mn ? idesc_bf16_mn(BMT, BN, true, B_MN) : idesc_bf16_mn(BMT, BN, false, B_MN);
+      const uint32_t step_a = a_mn ? 128 : 2;  // 16 of K, in 16-byte units
+      constexpr uint32_t kStepB = B_MN ? 128 : 2;
       const uint32_t full_bar = smem_u32(full), empty_bar = smem_u32(empty), tfull_bar = smem_u32(tfull), tempty_bar = smem_u32(tempty);
-      const uint64_t adesc0 = sdesc_sw128(smem_u32(smem), A_MN ? kAtom : 16, 1024);
+      const uint64_t adesc0 = sdesc_sw128(smem_u32(smem), a_mn ? kAtom : 16, 1024);
       const uint64_t bdesc0 = sdesc_sw128(smem_u32(smem) + KPS * a_bytes, B_MN ? kAtom : 16, 1024);
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
@@ -502,12 +517,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < KPS; ++j) {
               // a step deeper: the next tile of a K-major operand, 64 rows on in an MN-major one
-              const uint64_t adesc = adesc0 + (at + (A_MN ? j * 512u : j * (a_bytes / 16)));
+              const uint64_t adesc = adesc0 + (at + (a_mn ? j * 512u : j * (a_bytes / 16)));
               const uint64_t bdesc = bdesc0 + (at + (B_MN ? j * 512u : j * (T::B_BYTES / 16u)));
 #pragma unroll
               for (int k = 0; k < BK / 16; ++k) {
                 const uint32_t accum = (kb > kb0 || j > 0 || k > 0) ? 1u : 0u;
-                mma_step<PAIR>(d_tmem, adesc + kStepA * k, bdesc + kStepB * k, idesc, accum);
+                mma_step<PAIR>(d_tmem, adesc + step_a * k, bdesc + kStepB * k, idesc, accum);
               }
             }
             commit_to<PAIR>(empty_bar + 8u * stage);
@@ -537,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------------ epilogue
     const int quad = warp & 3;           // TMEM lanes [32 quad, 32 quad + 32) belong to this warp
     const int half = (warp - 2) >> 2;    // column groups half, half + 2, ...
-    const LinearEpilogue& e = p.e;
+    const LinearEpilogue& e = job.e;
     constexpr int NG = BN / 32;
     uint8_t* box = smem + T::OFF_STAGING + (warp - 2) * kBoxBytes;
     float* bias_s = reinterpret_cast<float*>(smem + T::OFF_STAGING + kEpiWarps * kBoxBytes + (warp - 2) * kBiasBytes);
@@ -547,17 +562,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (PAIR || ks == 1) {
       for (int t = t_first; t < tiles; t += t_step) {
         int mt, nt;
-        tile_at(p, t, mt, nt);
+        tile_at(job, t, mt, nt);
         const int row0 = mt * BMT + static_cast<int>(rank) * BM + quad * 32;
         const int n0 = nt * BN;
-        if (A_MN && p.cs.out && nt == 0) sum_columns(p, mt * BMT + static_cast<int>(rank) * BM);
+        if (!FWD && a_mn && p.cs.out && nt == 0) sum_columns(p.cs, job.M, mt * BMT + static_cast<int>(rank) * BM);
         uint4 res[4];
-        if (FWD && e.residual) fetch_box(e.residual, e.ld_residual, row0, n0 + 32 * half, p.M, p.N, e.vec_io, lane, res);
+        if (FWD && e.residual) fetch_box(e.residual, e.ld_residual, row0, n0 + 32 * half, job.M, job.N, e.vec_io, lane, res);
         if (FWD && e.bias) {  // this warp's columns, under the main loop
 #pragma unroll
           for (int g = half; g < NG; g += 2) {
             const int c = n0 + 32 * g + lane;
-            bias_s[16 * (g - half) + lane] = c < p.N ? e.bias[c] : 0.0f;
+            bias_s[16 * (g - half) + lane] = c < job.N ? e.bias[c] : 0.0f;
           }
           __syncwarp();
         }
@@ -572,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (FWD && e.residual) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) *box_at(box, (lane >> 2) + 8 * i, lane & 3) = res[i];
-            if (g + 2 < NG) fetch_box(e.residual, e.ld_residual, row0, n0 + 32 * (g + 2), p.M, p.N, e.vec_io, lane, res);
+            if (g + 2 < NG) fetch_box(e.residual, e.ld_residual, row0, n0 + 32 * (g + 2), job.M, job.N, e.vec_io, lane, res);
             __syncwarp();
           }
           float v[32];
@@ -606,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int c = 0; c < 4; ++c) *box_at(box, lane, c) = pack8(v + 8 * c);
               __syncwarp();
-              store_box(e.z, e.ld_z, row0, col0, p.M, p.N, e.vec_io, lane, box);
+              store_box(e.z, e.ld_z, row0, col0, job.M, job.N, e.vec_io, lane, box);
               __syncwarp();
             }
             if (e.act == DSV4V_ACT_GELU) {
@@ -631,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < 4; ++c) *box_at(box, lane, c) = pack8(v + 8 * c);
           __syncwarp();
-          store_box(e.y, e.ld_y, row0, col0, p.M, p.N, e.vec_io, lane, box);
+          store_box(e.y, e.ld_y, row0, col0, job.M, job.N, e.vec_io, lane, box);
           __syncwarp();
         }
         if (++acc == 2) {
@@ -643,10 +658,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Cluster split-K: one tile a cluster.  The partial goes to the ring, which the MMAs are
       // done with; only rows that exist are kept.
       int mt, nt;
-      tile_at(p, t_first, mt, nt);
+      tile_at(job, t_first, mt, nt);
       const int m0 = mt * BM, n0 = nt * BN;
-      const int rows = min(BM, p.M - m0);
-      if (A_MN && p.cs.out && nt == 0 && slice == 0) sum_columns(p, m0);
+      const int rows = min(BM, job.M - m0);
+      if (!FWD && a_mn && p.cs.out && nt == 0 && slice == 0) sum_columns(p.cs, job.M, m0);
       const bool got = mbar_wait(&tfull[0], 0, abort_flag, p.err, kErrTimeoutEpilogue);
       const bool all_got = __all_sync(0xffffffffu, got);
       tc_fence_after_sync();
@@ -671,9 +686,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       cluster_sync();
-      if (ks == 2) finish_pieces<BN, FWD, 2>(p, part, slice, rows, m0, n0);
-      else if (ks == 4) finish_pieces<BN, FWD, 4>(p, part, slice, rows, m0, n0);
-      else finish_pieces<BN, FWD, 8>(p, part, slice, rows, m0, n0);
+      if (ks == 2) finish_pieces<BN, FWD, 2>(job, part, slice, rows, m0, n0);
+      else if (ks == 4) finish_pieces<BN, FWD, 4>(job, part, slice, rows, m0, n0);
+      else finish_pieces<BN, FWD, 8>(job, part, slice, rows, m0, n0);
       __syncwarp();
       cluster_sync();  // no CTA leaves while another still reads its partial
     }
@@ -692,10 +707,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int BN, bool PAIR, bool A_MN, bool B_MN, bool FWD>
-cudaError_t launch_tile(const LinearPlan& plan, const CUtensorMap& ta, const CUtensorMap& tb, const Params& p, cudaStream_t s) {
+template <int BN, bool PAIR, LinearForm FORM>
+cudaError_t launch_tile(const LinearPlan& plan, const LinearMaps& t, const Params& p, cudaStream_t s) {
   using T = Tile<BN, PAIR>;
-  auto kern = k_linear<BN, PAIR, A_MN, B_MN, FWD>;
+  auto kern = k_linear<BN, PAIR, FORM>;
   static thread_local uint64_t ready = 0;  // devices on which the shared-memory limit is raised
   int dev = 0;
   if (cudaError_t e = cudaGetDevice(&dev)) return e;
@@ -704,23 +719,26 @@ cudaError_t launch_tile(const LinearPlan& plan, const CUtensorMap& ta, const CUt
     if (dev < 64) ready |= uint64_t(1) << dev;
   }
   const unsigned span = PAIR ? 2u : static_cast<unsigned>(plan.ks);
-  if (span == 1) return launch_pdl(kern, dim3(plan.grid), dim3(kThreads), T::SMEM, s, ta, tb, p, 1);
-  return launch_pdl_cluster(kern, dim3(plan.grid), dim3(kThreads), T::SMEM, s, span, ta, tb, p, PAIR ? 1 : plan.ks);
+  const int second = FORM == LINEAR_BOTH_GRADS ? 1 : 0;
+  if (span == 1)
+    return launch_pdl(kern, dim3(plan.grid), dim3(kThreads), T::SMEM, s, t.a[0], t.b[0], t.a[second], t.b[second], p, 1);
+  return launch_pdl_cluster(kern, dim3(plan.grid), dim3(kThreads), T::SMEM, s, span, t.a[0], t.b[0], t.a[second], t.b[second], p,
+                            PAIR ? 1 : plan.ks);
 }
 
-template <bool A_MN, bool B_MN, bool FWD>
-cudaError_t launch_form(const LinearPlan& plan, const CUtensorMap& ta, const CUtensorMap& tb, const Params& p, cudaStream_t s) {
+template <LinearForm FORM>
+cudaError_t launch_form(const LinearPlan& plan, const LinearMaps& t, const Params& p, cudaStream_t s) {
   if (plan.pair) {
-    if constexpr (!B_MN) {
-      if (plan.bn == 192) return launch_tile<192, true, A_MN, B_MN, FWD>(plan, ta, tb, p, s);
+    if constexpr (FORM == LINEAR_FORWARD) {
+      if (plan.bn == 192) return launch_tile<192, true, FORM>(plan, t, p, s);
     }
-    if (plan.bn == 128) return launch_tile<128, true, A_MN, B_MN, FWD>(plan, ta, tb, p, s);
-    if (plan.bn == 256) return launch_tile<256, true, A_MN, B_MN, FWD>(plan, ta, tb, p, s);
+    if (plan.bn == 128) return launch_tile<128, true, FORM>(plan, t, p, s);
+    if (plan.bn == 256) return launch_tile<256, true, FORM>(plan, t, p, s);
     return cudaErrorInvalidValue;
   }
-  if (plan.bn == 64) return launch_tile<64, false, A_MN, B_MN, FWD>(plan, ta, tb, p, s);
-  if (plan.bn == 128) return launch_tile<128, false, A_MN, B_MN, FWD>(plan, ta, tb, p, s);
-  if (plan.bn == 256) return launch_tile<256, false, A_MN, B_MN, FWD>(plan, ta, tb, p, s);
+  if (plan.bn == 64) return launch_tile<64, false, FORM>(plan, t, p, s);
+  if (plan.bn == 128) return launch_tile<128, false, FORM>(plan, t, p, s);
+  if (plan.bn == 256) return launch_tile<256, false, FORM>(plan, t, p, s);
   return cudaErrorInvalidValue;
 }
 
@@ -867,71 +885,133 @@ cudaError_t launch_linear_few(const void* x, int64_t ld_x, const void* w, int64_
   return launch_few<4, 2>(x, ld_x, w, ld_w, M, N, K, e, sms, s);
 }
 
+namespace {
+
+// Microseconds, fitted to every tile and split at 25 shapes of each form (1 to 8000 rows, widths 64
+// to 4608): the plan with the least estimate runs within 0.9% of the fastest one on average, 11% at
+// worst.  A stage takes the longest of its hand-over, its MMAs and its bytes into the SM; an
+// epilogue runs under the next tile's stages where there is one; clusters stay inside a GPC, so
+// that fewer of the larger ones fit (33 of 4 CTAs and 15 of 8, of 148 SMs).
+constexpr double kStart = 1.8, kPairStart = 0.87, kHandOver = 0.314, kMma = 0.035, kMmaColumn = 0.0011, kBytes = 132e3,
+                 kEpilogue = 0.27, kColumn = 0.0207, kPlainColumn = 0.0074, kTile = 0.22, kPairTile = 0.75, kSplit = 1.48,
+                 kSplitColumn = 0.0145, kSplitRank = 0.009;
+
+// The tiles of a product D[M, N] over a contraction of K, and their times.
+struct Tiling {
+  int64_t tm, tn, tiles, kb;
+  double stage, epilogue;
+  Tiling(const LinearPlan& p, LinearForm form, int64_t M, int64_t N, int64_t K) {
+    const int64_t bm = p.pair ? 2 * BM : BM;
+    const int steps = linear_depth(p) / BK;
+    tm = (M + bm - 1) / bm;
+    tn = (N + p.bn - 1) / p.bn;
+    tiles = tm * tn;
+    kb = (K + linear_depth(p) - 1) / linear_depth(p);
+    stage = std::max({kHandOver, steps * (kMma + kMmaColumn * p.bn), steps * (p.a_rows + (p.pair ? p.bn / 2 : p.bn)) * 128 / kBytes});
+    epilogue = kEpilogue + (form == LINEAR_FORWARD ? kColumn : kPlainColumn) * p.bn;
+  }
+  // Time of all tiles on `slots` CTAs (pairs, clusters of ks).
+  double time(const LinearPlan& p, int64_t slots, int ks, double finish) const {
+    const int64_t waves = (tiles + slots - 1) / slots;
+    const double main = stage * static_cast<double>((kb + ks - 1) / ks);
+    return kStart + p.pair * kPairStart + main + (waves - 1) * (std::max(main, finish) + kTile + p.pair * kPairTile) + finish;
+  }
+};
+
+bool tile_exists(bool pair, int bn, LinearForm form) {
+  return pair ? bn != 64 && (bn != 192 || form == LINEAR_FORWARD) : bn != 192;
+}
+
+}  // namespace
+
 LinearPlan plan_linear(LinearForm form, int64_t M, int64_t N, int64_t K, int sms) {
-  // Microseconds, fitted to every tile and split at 25 shapes of each form (1 to 8000 rows, widths 64
-  // to 4608): the plan with the least estimate runs within 0.6% of the fastest one on average, 11% at
-  // worst.  A stage takes the longest of its hand-over, its MMAs and its bytes into the SM; an
-  // epilogue runs under the next tile's stages where there is one; clusters stay inside a GPC, so
-  // that fewer of the larger ones fit (33 of 4 CTAs and 15 of 8, of 148 SMs).
-  constexpr double kStart = 1.8, kPairStart = 0.87, kHandOver = 0.314, kMma = 0.035, kMmaColumn = 0.0011, kBytes = 132e3,
-                   kEpilogue = 0.27, kColumn = 0.0207, kPlainColumn = 0.0074, kTile = 0.22, kPairTile = 0.75, kSplit = 1.48,
-                   kSplitColumn = 0.0145, kSplitRank = 0.009;
-  const bool a_mn = form == LINEAR_WEIGHT_GRAD, b_mn = form != LINEAR_FORWARD;
   LinearPlan best;
-  double best_cost = 1e300;
   for (int pair = 1; pair >= 0; --pair)
     for (int bn : {256, 192, 128, 64}) {
-      if (pair ? (bn == 64 || (bn == 192 && b_mn)) : bn == 192) continue;
-      const int64_t bm = pair ? 2 * BM : BM, tm = (M + bm - 1) / bm, tn = (N + bn - 1) / bn, tiles = tm * tn;
-      if (tiles > (int64_t(1) << 30)) continue;
+      if (!tile_exists(pair, bn, form)) continue;
       LinearPlan p;
       p.pair = pair;
       p.bn = bn;
-      p.a_rows = pair || a_mn ? BM : static_cast<int>(std::min<int64_t>(BM, (M + 7) / 8 * 8));
-      const int steps = linear_depth(p) / BK;
-      const int64_t kb = (K + linear_depth(p) - 1) / linear_depth(p);
-      const double stage = std::max({kHandOver, steps * (kMma + kMmaColumn * bn), steps * (p.a_rows + (pair ? bn / 2 : bn)) * 128 / kBytes});
+      p.a_rows = pair || form == LINEAR_WEIGHT_GRAD ? BM : static_cast<int>(std::min<int64_t>(BM, (M + 7) / 8 * 8));
+      const Tiling t(p, form, M, N, K);
+      if (t.tiles > (int64_t(1) << 30)) continue;
       for (int ks = 1; ks <= (pair ? 1 : 8); ks *= 2) {
         const int64_t slots = ks == 4 ? sms * 33 / 148 : (ks == 8 ? sms * 15 / 148 : sms / (pair ? 2 : ks));
-        if (slots < 1 || (ks > 1 && (tiles > slots || kb < 2 * ks))) break;
-        const int64_t waves = (tiles + slots - 1) / slots;
-        const double main = stage * static_cast<double>((kb + ks - 1) / ks);
-        double epilogue = kEpilogue + (form == LINEAR_FORWARD ? kColumn : kPlainColumn) * bn;
-        if (ks > 1) epilogue = kSplit + (kSplitColumn + kSplitRank * ks) * bn * static_cast<double>(std::min<int64_t>(M, BM)) / BM;
-        const double cost = kStart + pair * kPairStart + main + (waves - 1) * (std::max(main, epilogue) + kTile + pair * kPairTile) + epilogue;
-        if (cost < best_cost) {
-          best_cost = cost;
-          best = p;
-          best.ks = ks;
-          best.tiles_m = static_cast<int>(tm);
-          best.tiles_n = static_cast<int>(tn);
-          best.kb_total = static_cast<int>(kb);
-          best.grid = static_cast<int>(pair ? 2 * std::min(tiles, slots) : (ks > 1 ? tiles * ks : std::min(tiles, slots)));
+        if (slots < 1 || (ks > 1 && (t.tiles > slots || t.kb < 2 * ks))) break;
+        double finish = t.epilogue;
+        if (ks > 1) finish = kSplit + (kSplitColumn + kSplitRank * ks) * bn * static_cast<double>(std::min<int64_t>(M, BM)) / BM;
+        const double us = t.time(p, slots, ks, finish);
+        if (best.bn && us >= best.us) continue;
+        best = p;
+        best.us = us;
+        best.ks = ks;
+        best.tiles_m[0] = static_cast<int>(t.tm);
+        best.tiles_n[0] = static_cast<int>(t.tn);
+        best.kb_total[0] = static_cast<int>(t.kb);
+        best.grid = static_cast<int>(pair ? 2 * std::min(t.tiles, slots) : (ks > 1 ? t.tiles * ks : std::min(t.tiles, slots)));
+      }
+    }
+  return best;
+}
+
+LinearPlan plan_linear_both(int64_t rows, int64_t in, int64_t out, int sms) {
+  LinearPlan best;
+  for (int pair = 1; pair >= 0; --pair)
+    for (int bn : {256, 128, 64}) {
+      if (!tile_exists(pair, bn, LINEAR_BOTH_GRADS)) continue;
+      LinearPlan p;
+      p.pair = pair;
+      p.bn = bn;
+      p.a_rows = BM;
+      const Tiling x(p, LINEAR_BOTH_GRADS, rows, in, out), w(p, LINEAR_BOTH_GRADS, out, in, rows);
+      if (x.tiles > (int64_t(1) << 30) || w.tiles > (int64_t(1) << 30)) continue;
+      const int64_t slots = sms / (pair ? 2 : 1);
+      // The input gradient in 1, 2, .. waves of its tiles, the weight gradient on the other CTAs.
+      int64_t last = 0;
+      for (int64_t waves = 1; waves <= 16; ++waves) {
+        const int64_t ux = (x.tiles + waves - 1) / waves, uw = std::min(w.tiles, slots - ux);
+        if (ux == last) break;
+        last = ux;
+        if (uw < 1) continue;
+        const double us = std::max(x.time(p, ux, 1, x.epilogue), w.time(p, uw, 1, w.epilogue));
+        if (best.bn && us >= best.us) continue;
+        best = p;
+        best.us = us;
+        best.units = static_cast<int>(ux);
+        best.grid = static_cast<int>((pair ? 2 : 1) * (ux + uw));
+        const Tiling* t[2] = {&x, &w};
+        for (int j = 0; j < 2; ++j) {
+          best.tiles_m[j] = static_cast<int>(t[j]->tm);
+          best.tiles_n[j] = static_cast<int>(t[j]->tn);
+          best.kb_total[j] = static_cast<int>(t[j]->kb);
         }
       }
     }
   return best;
 }
 
-cudaError_t launch_linear(LinearForm form, const LinearPlan& plan, const CUtensorMap& ta, const CUtensorMap& tb, int M, int N,
-                          const LinearEpilogue& e, const ColumnSums& cs, uint32_t* err, cudaStream_t s) {
+cudaError_t launch_linear(LinearForm form, const LinearPlan& plan, const LinearMaps& maps, const LinearProduct* products,
+                          const ColumnSums& cs, uint32_t* err, cudaStream_t s) {
   Params p{};
-  p.cs = cs;
-  p.M = M;
-  p.N = N;
-  p.tiles_m = plan.tiles_m;
-  p.tiles_n = plan.tiles_n;
-  p.kb_total = plan.kb_total;
+  for (int j = 0; j < (form == LINEAR_BOTH_GRADS ? 2 : 1); ++j) {
+    Job& job = p.job[j];
+    job.M = products[j].M;
+    job.N = products[j].N;
+    job.e = products[j].e;
+    job.tiles_m = plan.tiles_m[j];
+    job.tiles_n = plan.tiles_n[j];
+    job.kb_total = plan.kb_total[j];
+  }
+  p.units = plan.units;
   p.a_rows = plan.a_rows;
-  const int kps = linear_depth(plan) / BK;
-  const int stage_bytes = kps * ((form == LINEAR_WEIGHT_GRAD ? BM : plan.a_rows) + (plan.pair ? plan.bn / 2 : plan.bn)) * BK * 2;
-  p.stages = std::min(kMaxStages, Tile<256, true>::RING / stage_bytes);
-  p.e = e;
+  p.stages = std::min(kMaxStages, Tile<256, true>::RING / (linear_depth(plan) * (plan.a_rows + (plan.pair ? plan.bn / 2 : plan.bn)) * 2));
+  p.cs = cs;
   p.err = err;
   switch (form) {
-    case LINEAR_FORWARD: return launch_form<false, false, true>(plan, ta, tb, p, s);
-    case LINEAR_INPUT_GRAD: return launch_form<false, true, false>(plan, ta, tb, p, s);
-    case LINEAR_WEIGHT_GRAD: return launch_form<true, true, false>(plan, ta, tb, p, s);
+    case LINEAR_FORWARD: return launch_form<LINEAR_FORWARD>(plan, maps, p, s);
+    case LINEAR_INPUT_GRAD: return launch_form<LINEAR_INPUT_GRAD>(plan, maps, p, s);
+    case LINEAR_WEIGHT_GRAD: return launch_form<LINEAR_WEIGHT_GRAD>(plan, maps, p, s);
+    case LINEAR_BOTH_GRADS: return launch_form<LINEAR_BOTH_GRADS>(plan, maps, p, s);
   }
   return cudaErrorInvalidValue;
 }

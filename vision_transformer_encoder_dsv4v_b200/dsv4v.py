@@ -548,11 +548,13 @@ class GradTable:
     def __init__(self, grads):
         self.tensors = list(grads)
         self.device = self.tensors[0].device if self.tensors else None
-        self.index = self.device.index if self.tensors else None
+        self.index = self.device.index if self.tensors and self.device.type == "cuda" else None
         self.n = len(self.tensors)
         self.c = (Grad * max(1, self.n))()
         for i, g in enumerate(self.tensors):
-            self.c[i] = Grad(_on_device(g, f"grads[{i}]", self.device), g.numel(), _dtype_code(g, f"grads[{i}]"))
+            if g.get_device() != self.index or not g.is_contiguous():
+                _on_device(g, f"grads[{i}]", self.device)
+            self.c[i] = Grad(g.data_ptr(), g.numel(), _dtype_code(g, "a gradient"))
 
 
 def dsv4v_grad_norm_workspace_size(table) -> int:
@@ -585,34 +587,37 @@ class AdamwTable:
         self.tensors = [dict(t) for t in tensors]
         self.n = len(self.tensors)
         self.device = self.tensors[0]["param"].device if self.n else None
-        self.index = self.device.index if self.n else None
+        self.index = self.device.index if self.n and self.device.type == "cuda" else None
         self.c = (AdamwTensor * max(1, self.n))()
         f32, codes, written = (torch.float32,), (torch.uint8, torch.float8_e4m3fn), []
-        any_float = (torch.float32, torch.bfloat16)
-        for i, t in enumerate(self.tensors):
-            n, eight = t["param"].numel(), t["exp_avg"].dtype in codes
-            blocks = (n + DSV4V_STATE_BLOCK - 1) // DSV4V_STATE_BLOCK
-            state = codes if eight else f32
+        any_float, index = (torch.float32, torch.bfloat16), self.index
 
-            def address(key, dtypes, numel, optional=False):
-                x = t.get(key)
-                if x is None:
-                    if optional:
-                        return None
-                    raise ValueError(f"tensors[{i}] has no {key}")
+        def address(i, t, key, dtypes, numel):
+            x = t.get(key)
+            if x is None:
+                raise ValueError(f"tensors[{i}] has no {key}")
+            if x.get_device() == index and x.dtype in dtypes and x.numel() == numel and x.is_contiguous():
+                ptr = x.data_ptr()
+            else:  # which of these it is
                 ptr = _on_device(x, f"tensors[{i}] {key}", self.device, dtypes, numel)
-                if numel and key != "grad":
-                    written.append((ptr, ptr + numel * x.element_size(), i))
-                return ptr
+            if numel and key != "grad":
+                written.append((ptr, ptr + numel * x.element_size(), i))
+            return ptr
 
-            if not eight and (t.get("exp_avg_scale") is not None or t.get("exp_avg_sq_scale") is not None):
+        for i, t in enumerate(self.tensors):
+            p, n = t["param"], t["param"].numel()
+            eight = t["exp_avg"].dtype in codes
+            state, m_scale, v_scale, master = codes if eight else f32, None, None, None
+            if eight:
+                blocks = (n + DSV4V_STATE_BLOCK - 1) // DSV4V_STATE_BLOCK
+                m_scale, v_scale = (address(i, t, key, f32, blocks) for key in ("exp_avg_scale", "exp_avg_sq_scale"))
+            elif t.get("exp_avg_scale") is not None or t.get("exp_avg_sq_scale") is not None:
                 raise ValueError(f"tensors[{i}] has scales, but fp32 states")
-            self.c[i] = AdamwTensor(address("param", any_float, n), address("grad", any_float, n),
-                                    address("master", f32, n, optional=True), address("exp_avg", state, n),
-                                    address("exp_avg_sq", state, n),
-                                    address("exp_avg_scale", f32, blocks) if eight else None,
-                                    address("exp_avg_sq_scale", f32, blocks) if eight else None, n,
-                                    _dtype_code(t["param"], "param"), _dtype_code(t["grad"], "grad"), 8 if eight else 32,
+            if t.get("master") is not None:
+                master = address(i, t, "master", f32, n)
+            self.c[i] = AdamwTensor(address(i, t, "param", any_float, n), address(i, t, "grad", any_float, n), master,
+                                    address(i, t, "exp_avg", state, n), address(i, t, "exp_avg_sq", state, n), m_scale,
+                                    v_scale, n, _dtype_code(p, "param"), _dtype_code(t["grad"], "grad"), 8 if eight else 32,
                                     float(t.get("weight_decay") or 0.0))
         written.sort()
         for (_, end, i), (begin, _, j) in zip(written, written[1:]):
