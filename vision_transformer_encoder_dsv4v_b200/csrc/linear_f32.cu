@@ -59,38 +59,37 @@ __device__ __forceinline__ void split8(const float (&x)[8], uint4 (&out)[3]) {
 }
 
 // A thread's share of an operand's ROWS x 64 part of a stage, in pieces of one row and eight
-// consecutive contraction indices.
+// consecutive contraction indices.  A thread's pieces are 64 rows (or, MN-major, 512 / ROWS pieces of
+// the contraction) apart.
 template <int ROWS, bool K_FAST>
 struct Share {
   static constexpr int PIECES = ROWS * 8 / kConvert;
-  const float* at[PIECES];  // the first element of the piece in the next stage
+  const float* at;  // the first element of piece 0 in the next stage
   int64_t ld;
-  int left[PIECES];         // contraction indices from there on (32 bits: at most 2^30 rows, see the limits); 0 outside the rows
-  bool vec;
+  bool vec, in[PIECES];  // 16-byte loads; rows that exist
   float x[PIECES][8];
 
   static __device__ __forceinline__ int row(int j) {
-    const int q = static_cast<int>(threadIdx.x) + kConvert * j;
-    return K_FAST ? q / 8 : q % ROWS;
+    const int t = static_cast<int>(threadIdx.x);
+    return K_FAST ? t / 8 + kConvert / 8 * j : t % ROWS;
   }
   static __device__ __forceinline__ int piece(int j) {
-    const int q = static_cast<int>(threadIdx.x) + kConvert * j;
-    return K_FAST ? q % 8 : q / ROWS;
+    const int t = static_cast<int>(threadIdx.x);
+    return K_FAST ? t % 8 : t / ROWS + kConvert / ROWS * j;
   }
-  // Rows i0 .. of n_i, contraction indices k0 .. of n_k.
-  __device__ __forceinline__ Share(const float* a, int64_t ld_, int64_t i0, int64_t n_i, int64_t k0, int64_t n_k) : ld(ld_) {
+  // Rows i0 .. of n_i, contraction indices from k0 on.
+  __device__ __forceinline__ Share(const float* a, int64_t ld_, int64_t i0, int64_t n_i, int64_t k0) : ld(ld_) {
     vec = (reinterpret_cast<uintptr_t>(a) & 15) == 0 && ld % 4 == 0;
+    const int64_t i = i0 + row(0), k = k0 + piece(0) * 8;
+    at = a + (K_FAST ? i * ld + k : k * ld + i);
 #pragma unroll
-    for (int j = 0; j < PIECES; ++j) {
-      const int64_t i = i0 + row(j), k = k0 + piece(j) * 8;
-      at[j] = a + (K_FAST ? i * ld + k : k * ld + i);
-      left[j] = i < n_i ? static_cast<int>(n_k - k) : 0;
-    }
+    for (int j = 0; j < PIECES; ++j) in[j] = i0 + row(j) < n_i;
   }
-  // Starts loading piece j of the next stage.
-  __device__ __forceinline__ void load(int j) {
-    const float* p = at[j];
-    if (left[j] >= 8 && (!K_FAST || vec)) {
+  // Starts loading piece j of the next stage, which `left` indices of the contraction remain for.
+  __device__ __forceinline__ void load(int j, int left) {
+    const float* p = at + (K_FAST ? kConvert / 8 : kConvert / ROWS * 8) * j * ld;
+    left = in[j] ? left - piece(j) * 8 : 0;
+    if (left >= 8 && (!K_FAST || vec)) {
       if constexpr (K_FAST) {
         const float4 lo = reinterpret_cast<const float4*>(p)[0], hi = reinterpret_cast<const float4*>(p)[1];
         x[j][0] = lo.x, x[j][1] = lo.y, x[j][2] = lo.z, x[j][3] = lo.w, x[j][4] = hi.x, x[j][5] = hi.y, x[j][6] = hi.z, x[j][7] = hi.w;
@@ -100,12 +99,11 @@ struct Share {
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[j][e] = e < left[j] ? p[K_FAST ? e : e * ld] : 0.0f;
+      for (int e = 0; e < 8; ++e) x[j][e] = e < left ? p[K_FAST ? e : e * ld] : 0.0f;
     }
-    at[j] += K_FAST ? TK : TK * ld;
-    left[j] -= TK;
   }
-  // Its parts into the operand's three tiles.
+  __device__ __forceinline__ void advance() { at += K_FAST ? TK : TK * ld; }
+  // The piece's parts into the operand's three tiles.
   __device__ __forceinline__ void store(int j, uint8_t* tiles) const {
     uint4 parts[3];
     split8(x[j], parts);
@@ -249,12 +247,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_f32(const float* a, int6
   }
   if (warp < kConvert / 32) {
     // ------------------------------------------------------------------ load and split, add up
-    Share<TM, A_K> pa(a, lda, m0, M, first * TK, K);
-    Share<TN, B_K> pb(b, ldb, n0, N, first * TK, K);
+    Share<TM, A_K> pa(a, lda, m0, M, first * TK);
+    Share<TN, B_K> pb(b, ldb, n0, N, first * TK);
+    int left = static_cast<int>(min(K - first * TK, int64_t(1) << 30));  // contraction indices from the next stage on
+    auto load_all = [&] {
 #pragma unroll
-    for (int j = 0; j < pa.PIECES; ++j) pa.load(j);
+      for (int j = 0; j < pa.PIECES; ++j) pa.load(j, left);
 #pragma unroll
-    for (int j = 0; j < pb.PIECES; ++j) pb.load(j);
+      for (int j = 0; j < pb.PIECES; ++j) pb.load(j, left);
+    };
+    load_all();
     // Rows 32 (warp % 4) + lane, columns 16 (warp / 4) ..
     const int quad = warp & 3, col = (warp >> 2) * 16;
     float v[16];
@@ -293,15 +295,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_f32(const float* a, int6
       if (!ok) break;
       uint8_t* to = smem + stage * kStageBytes;
       // a piece's next loads start as soon as it is split
+      left -= TK;
+      pa.advance();
+      pb.advance();
 #pragma unroll
       for (int j = 0; j < pa.PIECES; ++j) {
         pa.store(j, to);
-        pa.load(j);
+        pa.load(j, left);
       }
 #pragma unroll
       for (int j = 0; j < pb.PIECES; ++j) {
         pb.store(j, to + 3 * kABytes);
-        pb.load(j);
+        pb.load(j, left);
       }
       fence_proxy_async_smem();
       __syncwarp();
