@@ -1,6 +1,7 @@
 // The Linear layer on tcgen05: y = act(x W^T + b) + r and, for its backward, dx = dz W and
-// dW = dz^T x.  One GEMM kernel D[M, N] = A . B^T serves the three; what differs is how the operands
-// lie in memory (K-major: rows of the contraction; MN-major: columns) and the epilogue.
+// dW = dz^T x.  One GEMM kernel D[M, N] = A . B^T serves the three, the two gradients also side by
+// side in one launch; what differs is how the operands lie in memory (K-major: rows of the
+// contraction; MN-major: columns) and the epilogue.
 //
 // Against the block's GEMM (gemm_tc.cu) this one takes any extent: TMA fills what lies outside the
 // tensors with zeros, and the epilogue stores row segments through shared memory, so that rows,
@@ -109,53 +110,61 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
 }
 
 // The instructions below are executed by a whole, converged warp and issued by one of its lanes
-// (always the same one): the election is part of the instruction's own predicate, not a branch.
-#define ELECTED(body) "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t" body "}"
+// (always the same one) if that lane's `ok` holds: both are part of the instruction's own predicate,
+// not a branch, which lanes whose waits ended differently could take differently.
+#define ELECTED(ok, body) "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.and.b32 q, " ok ", 0, q;\n\t" body "}"
 
-__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
-  asm volatile(ELECTED("@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t") ::"r"(bar), "r"(bytes) : "memory");
+__device__ __forceinline__ bool elected() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes, uint32_t ok) {
+  asm volatile(ELECTED("%2", "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t") ::"r"(bar), "r"(bytes), "r"(ok) : "memory");
 }
 
 // Tiled load of one box at (x, y) into this CTA's shared memory, counted on the barrier at `bar`
 // (PAIR: a shared::cluster address, the leader's).
 template <bool PAIR>
-__device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+__device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, uint32_t ok) {
   if constexpr (PAIR)
-    asm volatile(ELECTED("@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-                         " [%0], [%1, {%3, %4}], [%2];\n\t") ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+    asm volatile(ELECTED("%5", "@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+                               " [%0], [%1, {%3, %4}], [%2];\n\t") ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(ok)
                  : "memory");
   else
-    asm volatile(ELECTED("@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-                         " [%0], [%1, {%3, %4}], [%2];\n\t") ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+    asm volatile(ELECTED("%5", "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                               " [%0], [%1, {%3, %4}], [%2];\n\t") ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(ok)
                  : "memory");
 }
 
 // D[tmem] (+)= A[smem] * B[smem]^T; PAIR: of both CTAs, M = 256.
 template <bool PAIR>
-__device__ __forceinline__ void mma_step(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_step(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate,
+                                         uint32_t ok) {
   if constexpr (PAIR)
-    asm volatile(ELECTED(".reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                         "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t") ::"r"(d_tmem),
-                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+    asm volatile(ELECTED("%5", ".reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                               "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t") ::"r"(d_tmem),
+                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(ok)
                  : "memory");
   else
-    asm volatile(ELECTED(".reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                         "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t") ::"r"(d_tmem),
-                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+    asm volatile(ELECTED("%5", ".reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                               "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t") ::"r"(d_tmem),
+                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(ok)
                  : "memory");
 }
 
 // Arrives on the barrier (PAIR: on both CTAs') when every MMA issued so far has completed.
 template <bool PAIR>
-__device__ __forceinline__ void commit_to(uint32_t bar) {
+__device__ __forceinline__ void commit_to(uint32_t bar, uint32_t ok) {
   if constexpr (PAIR)
-    asm volatile(ELECTED("@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t") ::"r"(bar),
-                 "h"(static_cast<uint16_t>(3))
+    asm volatile(ELECTED("%2", "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t") ::"r"(bar),
+                 "h"(static_cast<uint16_t>(3)), "r"(ok)
                  : "memory");
   else
-    asm volatile(ELECTED("@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t") ::"r"(bar) : "memory");
+    asm volatile(ELECTED("%1", "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t") ::"r"(bar), "r"(ok) : "memory");
 }
 
 // One product of a launch.
@@ -452,24 +461,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n0 = nt * BN + static_cast<int>(rank) * (BN / 2) * (PAIR ? 1 : 0);
       for (int kb = kb0; kb < kb1; ++kb) {
         ok = ok && bar_wait(empty_bar + 8u * stage, phase ^ 1, abort_flag, p.err, kErrTimeoutProducer);
+        const uint32_t sa = ring + static_cast<uint32_t>(stage) * stage_bytes, sb = sa + KPS * a_bytes, bar = full_leader + 8u * stage;
+        if (posts) bar_expect(full_bar + 8u * stage, tx, ok);
+        const int k0 = kb * (KPS * BK);
+        if (a_mn) {
+#pragma unroll
+          for (int j = 0; j < BM / 64; ++j) tma_tile<PAIR>(sa + j * kAtom, tm_a, bar, m0 + 64 * j, k0, ok);
+        } else {
+#pragma unroll
+          for (int j = 0; j < KPS; ++j) tma_tile<PAIR>(sa + j * a_bytes, tm_a, bar, k0 + j * BK, m0, ok);
+        }
+        if constexpr (B_MN) {
+#pragma unroll
+          for (int j = 0; j < T::B_ROWS / 64; ++j) tma_tile<PAIR>(sb + j * kAtom, tm_b, bar, n0 + 64 * j, k0, ok);
+        } else {
+#pragma unroll
+          for (int j = 0; j < KPS; ++j) tma_tile<PAIR>(sb + j * T::B_BYTES, tm_b, bar, k0 + j * BK, n0, ok);
+        }
         if (ok) {
-          const uint32_t sa = ring + static_cast<uint32_t>(stage) * stage_bytes, sb = sa + KPS * a_bytes, bar = full_leader + 8u * stage;
-          if (posts) bar_expect(full_bar + 8u * stage, tx);
-          const int k0 = kb * (KPS * BK);
-          if (a_mn) {
-#pragma unroll
-            for (int j = 0; j < BM / 64; ++j) tma_tile<PAIR>(sa + j * kAtom, tm_a, bar, m0 + 64 * j, k0);
-          } else {
-#pragma unroll
-            for (int j = 0; j < KPS; ++j) tma_tile<PAIR>(sa + j * a_bytes, tm_a, bar, k0 + j * BK, m0);
-          }
-          if constexpr (B_MN) {
-#pragma unroll
-            for (int j = 0; j < T::B_ROWS / 64; ++j) tma_tile<PAIR>(sb + j * kAtom, tm_b, bar, n0 + 64 * j, k0);
-          } else {
-#pragma unroll
-            for (int j = 0; j < KPS; ++j) tma_tile<PAIR>(sb + j * T::B_BYTES, tm_b, bar, k0 + j * BK, n0);
-          }
           issued |= 1u << stage;
           issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
         }
@@ -482,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // No copy is in flight when the CTA exits: the MMAs consumed every stage, unless a wait gave
     // up; then wait for each one here.  The second CTA of a pair has no full barrier of its own
     // and waits for the MMAs' release of the stages that it filled.
-    if (lane == 0) {
+    if (elected()) {
       volatile int never = 0;
       for (int s = 0; s < p.stages; ++s) {
         if (!(issued & (1u << s))) continue;
@@ -513,33 +522,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = ok && bar_wait(full_bar + 8u * stage, phase, abort_flag, p.err, kErrTimeoutMma);
           tc_fence_after_sync();
           const uint32_t at = static_cast<uint32_t>(stage) * (stage_bytes / 16);
-          if (ok) {
 #pragma unroll
-            for (int j = 0; j < KPS; ++j) {
-              // a step deeper: the next tile of a K-major operand, 64 rows on in an MN-major one
-              const uint64_t adesc = adesc0 + (at + (a_mn ? j * 512u : j * (a_bytes / 16)));
-              const uint64_t bdesc = bdesc0 + (at + (B_MN ? j * 512u : j * (T::B_BYTES / 16u)));
+          for (int j = 0; j < KPS; ++j) {
+            // a step deeper: the next tile of a K-major operand, 64 rows on in an MN-major one
+            const uint64_t adesc = adesc0 + (at + (a_mn ? j * 512u : j * (a_bytes / 16)));
+            const uint64_t bdesc = bdesc0 + (at + (B_MN ? j * 512u : j * (T::B_BYTES / 16u)));
 #pragma unroll
-              for (int k = 0; k < BK / 16; ++k) {
-                const uint32_t accum = (kb > kb0 || j > 0 || k > 0) ? 1u : 0u;
-                mma_step<PAIR>(d_tmem, adesc + step_a * k, bdesc + kStepB * k, idesc, accum);
-              }
+            for (int k = 0; k < BK / 16; ++k) {
+              const uint32_t accum = (kb > kb0 || j > 0 || k > 0) ? 1u : 0u;
+              mma_step<PAIR>(d_tmem, adesc + step_a * k, bdesc + kStepB * k, idesc, accum, ok);
             }
-            commit_to<PAIR>(empty_bar + 8u * stage);
           }
+          commit_to<PAIR>(empty_bar + 8u * stage, ok);
           if (++stage == p.stages) {
             stage = 0;
             phase ^= 1;
           }
         }
-        if (ok) commit_to<PAIR>(tfull_bar + 8u * acc);
+        commit_to<PAIR>(tfull_bar + 8u * acc, ok);
         if (++acc == 2) {
           acc = 0;
           acc_phase ^= 1;
         }
       }
       // Every MMA issued completes before TMEM is released.
-      commit_to<PAIR>(smem_u32(mma_done));
+      commit_to<PAIR>(smem_u32(mma_done), 1u);
       volatile int never = 0;
       mbar_wait(mma_done, 0, &never, p.err, kErrTimeoutMma);
     }
