@@ -200,22 +200,44 @@ __device__ __forceinline__ void tile_at(const Job& p, int t, int& m, int& n) {
 // an element keep a tile's epilogue under its main loop, which erff and expf would not (about 30
 // instructions an element: 10,000 clocks a 128 x 256 tile).
 //
-// erf by Abramowitz and Stegun 7.1.26, |error| <= 1.5e-7: erfc(x) = poly(t) e^(-x^2), x >= 0.
-__device__ __forceinline__ float gelu_fast(float z) {
-  const float x = fabsf(z) * 0.70710678118654752f;
-  const float t = rcp_approx(fmaf(0.3275911f, x, 1.0f));
-  float q = fmaf(1.061405429f, t, -1.453152027f);
-  q = fmaf(q, t, 1.421413741f);
-  q = fmaf(q, t, -0.284496736f);
-  q = fmaf(q, t, 0.254829592f);
-  const float tail = 0.5f * q * t * ex2_approx(x * x * -1.4426950408889634f);  // (1 - erf) / 2 at |x|
-  return z * (z >= 0.0f ? 1.0f - tail : tail);
+// erf by Abramowitz and Stegun 7.1.26, |error| <= 1.5e-7: erfc(x) = poly(t) e^(-x^2), x >= 0.  Two
+// values at a time, in packed fp32 instructions, which halves the issue slots that bound it (784 x
+// 1024 x 2816, GELU: 13.5 -> 13.1 us).
+__device__ __forceinline__ uint64_t both(float v) { return pk2(v, v); }
+__device__ __forceinline__ void gelu_fast(float& a, float& b) {
+  const uint64_t x = mul2(pk2(fabsf(a), fabsf(b)), both(0.70710678118654752f));
+  const uint64_t e = mul2(mul2(x, x), both(-1.4426950408889634f));
+  float t0, t1, e0, e1;
+  upk2(fma2(both(0.3275911f), x, both(1.0f)), t0, t1);
+  upk2(e, e0, e1);
+  const uint64_t t = pk2(rcp_approx(t0), rcp_approx(t1));
+  uint64_t q = fma2(both(1.061405429f * 0.5f), t, both(-1.453152027f * 0.5f));
+  q = fma2(q, t, both(1.421413741f * 0.5f));
+  q = fma2(q, t, both(-0.284496736f * 0.5f));
+  q = fma2(q, t, both(0.254829592f * 0.5f));
+  const uint64_t tail = mul2(mul2(q, t), pk2(ex2_approx(e0), ex2_approx(e1)));  // (1 - erf) / 2 at |x|
+  float l0, l1, h0, h1;
+  upk2(tail, l0, l1);
+  upk2(sub2(both(1.0f), tail), h0, h1);
+  upk2(mul2(pk2(a, b), pk2(a >= 0.0f ? h0 : l0, b >= 0.0f ? h1 : l1)), a, b);
 }
-__device__ __forceinline__ float silu_fast(float z) {
-  return z * rcp_approx(1.0f + ex2_approx(z * -1.4426950408889634f));
+__device__ __forceinline__ void silu_fast(float& a, float& b) {
+  float e0, e1, d0, d1;
+  const uint64_t z = pk2(a, b);
+  upk2(mul2(z, both(-1.4426950408889634f)), e0, e1);
+  upk2(add2(both(1.0f), pk2(ex2_approx(e0), ex2_approx(e1))), d0, d1);
+  upk2(mul2(z, pk2(rcp_approx(d0), rcp_approx(d1))), a, b);
 }
-__device__ __forceinline__ float activate(float z, int act) {
-  return act == DSV4V_ACT_GELU ? gelu_fast(z) : (act == DSV4V_ACT_SILU ? silu_fast(z) : z);
+// An even number of values.
+template <int N>
+__device__ __forceinline__ void activate(float (&v)[N], int act) {
+  if (act == DSV4V_ACT_GELU) {
+#pragma unroll
+    for (int j = 0; j < N; j += 2) gelu_fast(v[j], v[j + 1]);
+  } else if (act == DSV4V_ACT_SILU) {
+#pragma unroll
+    for (int j = 0; j < N; j += 2) silu_fast(v[j], v[j + 1]);
+  }
 }
 
 // 16-byte chunk `c` (0..3) of row `r` of a staging box: 32 rows of 64 bytes.  Eight lanes that
@@ -336,8 +358,7 @@ __device__ __forceinline__ void finish_pieces(const Job& p, float* part, int sli
           if (j < n) v[j] += e.bias[col + j];
       }
       if (e.z) put(e.z + static_cast<int64_t>(row) * e.ld_z + col);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = activate(v[j], e.act);
+      activate(v, e.act);
       if (e.residual) {
         const __nv_bfloat16* r = e.residual + static_cast<int64_t>(row) * e.ld_residual + col;
         if (whole) {
@@ -631,13 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               store_box(e.z, e.ld_z, row0, col0, job.M, job.N, e.vec_io, lane, box);
               __syncwarp();
             }
-            if (e.act == DSV4V_ACT_GELU) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = gelu_fast(v[j]);
-            } else if (e.act == DSV4V_ACT_SILU) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = silu_fast(v[j]);
-            }
+            activate(v, e.act);
             if (e.residual) {
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
@@ -863,7 +878,9 @@ __global__ void __launch_bounds__(kFewThreads, F == 1 ? 4 : 2) k_linear_few(cons
     if (row < rows && col < N) {
       if (e.bias) v += e.bias[col];
       if (e.z) e.z[row * e.ld_z + col] = __float2bfloat16_rn(v);
-      v = activate(v, e.act);
+      float two[2] = {v, 0.0f};
+      activate(two, e.act);
+      v = two[0];
       if (e.residual) v += __bfloat162float(e.residual[row * e.ld_residual + col]);
       e.y[row * e.ld_y + col] = __float2bfloat16_rn(v);
     }
