@@ -104,7 +104,8 @@ def run_forward(kind, rows, k, n, act, bias=True, residual=True, save_z=True, in
 # sums), whole tiles, pairs; extents on, before and behind a tile's edge.
 SHAPES = [(1, 1, 1), (1, 8, 3), (1, 4608, 4608), (2, 64, 7), (3, 2816, 64), (5, 9, 1000), (8, 1024, 2816), (17, 63, 129),
           (64, 4096, 512), (127, 65, 255), (128, 64, 64), (129, 128, 257), (200, 588, 1001), (255, 1000, 96), (784, 1024, 1024),
-          (777, 588, 1001), (784, 1024, 2816), (1025, 200, 2100), (2500, 72, 1155), (4100, 130, 2100)]
+          (777, 588, 1001), (784, 1024, 2816), (1025, 200, 2100), (2500, 72, 1155), (4100, 130, 2100),
+          (1144, 72, 2055), (1355, 264, 1861), (2858, 1864, 1872)]
 
 
 @pytest.mark.parametrize("rows,k,n", SHAPES)
