@@ -14,9 +14,11 @@
 // Roles (544 threads): warps 0 to 15 load fp32, split it and write the parts into a 3-stage ring
 // (K-major, 128-byte swizzle, transposing where the contraction is not contiguous), and add up the
 // accumulators, 16 columns each; warp 16 issues the MMAs.  All store the 128 x 64 tile at the end.
-// Loading and splitting bounds it, then the MMAs.  Where there are fewer tiles than SMs, two to eight
-// CTAs of a cluster share one, each with a part of the contraction; a rank stores its share of the
-// rows and fetches the others' sums through distributed shared memory, in rank order.
+// A stage takes 1.2 us: about 390 instructions a thread, and 220 KB through shared memory and L1 (parts
+// stored 74, read by the MMAs 98, loads 49); the MMAs alone need half of that.  Where there are fewer
+// tiles than SMs, two to eight CTAs of a cluster share one, each with a part of the contraction; a
+// rank stores its share of the rows and fetches the others' sums through distributed shared memory,
+// in rank order.
 #include <algorithm>
 
 #include "common.cuh"
