@@ -440,6 +440,8 @@ def _matrix(t, what, rows, cols, ld, dtype, device):
         return None
     ld = ld or cols
     if t.dtype is dtype and t.get_device() == device and t.shape == (rows, cols):
+        if ld == cols and t.is_contiguous():
+            return t.data_ptr()
         step = t.stride()
         if (step[0] == ld or rows <= 1) and (step[1] == 1 or cols <= 1):
             return t.data_ptr()
@@ -452,28 +454,43 @@ def _matrix(t, what, rows, cols, ld, dtype, device):
     raise ValueError(f"{what} has strides {t.stride()}, not {(ld, 1)}")
 
 
+_dtypes, _raw_stream_of = {}, None  # torch's, looked up once
+
+
 def _layer_dtype(layer):
-    import torch
-    return torch.bfloat16 if layer.dtype == DSV4V_BF16 else torch.float32
+    if not _dtypes:
+        import torch
+        _dtypes.update({DSV4V_F32: torch.float32, DSV4V_BF16: torch.bfloat16})
+    return _dtypes.get(layer.dtype, _dtypes[DSV4V_F32])
 
 
 def _raw_stream(stream, device):
-    import torch
-    return stream if stream is not None else torch._C._cuda_getCurrentRawStream(device)
+    global _raw_stream_of
+    if stream is not None:
+        return stream
+    if _raw_stream_of is None:
+        import torch
+        _raw_stream_of = torch._C._cuda_getCurrentRawStream
+    return _raw_stream_of(device)
 
 
 def _vector(t, what, n, device):
     import torch
-    return None if t is None else _on_device(t, what, torch.device("cuda", device), (torch.float32,), n)
+    if t is None:
+        return None
+    if t.dtype is torch.float32 and t.get_device() == device and t.numel() == n and t.is_contiguous():
+        return t.data_ptr()
+    return _on_device(t, what, torch.device("cuda", device), (torch.float32,), n)
 
 
 def dsv4v_linear_forward(layer: Linear, x, w, bias, residual, z, y, stream=None):
     """y = act(x . w^T + bias) + residual; z (the activation's input), bias and residual may be None."""
     m, k, n, dtype, device = layer.rows, layer.in_features, layer.out_features, _layer_dtype(layer), _device_index()
     _check(lib().dsv4v_linear_forward(ctypes.byref(layer), _matrix(x, "x", m, k, layer.ld_x, dtype, device),
-                                      _matrix(w, "w", n, k, layer.ld_w, dtype, device), _vector(bias, "bias", n, device),
-                                      _matrix(residual, "residual", m, n, layer.ld_residual, dtype, device),
-                                      _matrix(z, "z", m, n, layer.ld_z, dtype, device),
+                                      _matrix(w, "w", n, k, layer.ld_w, dtype, device),
+                                      None if bias is None else _vector(bias, "bias", n, device),
+                                      None if residual is None else _matrix(residual, "residual", m, n, layer.ld_residual, dtype, device),
+                                      None if z is None else _matrix(z, "z", m, n, layer.ld_z, dtype, device),
                                       _matrix(y, "y", m, n, layer.ld_y, dtype, device), _raw_stream(stream, device)),
            "dsv4v_linear_forward")
 
@@ -518,10 +535,19 @@ def _on_device(t, what, device, dtypes=None, numel=None):
     return t.data_ptr()
 
 
+_get_device = None  # torch's, once CUDA is up
+
+
 def _device_index():
     """The current CUDA device's index (-1 without one)."""
-    import torch
-    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else (torch.cuda.current_device() if torch.cuda.is_available() else -1)
+    global _get_device
+    if _get_device is None:
+        import torch
+        if not torch.cuda.is_available():
+            return -1
+        torch.cuda.init()
+        _get_device = torch._C._cuda_getDevice
+    return _get_device()
 
 
 def _current(table, where):
