@@ -144,8 +144,17 @@ def test_linear_forward_strides(kind, rows, k, n, ld_y, offset):
     run_forward(kind, rows, k, n, "gelu", ld_x=pad8(k) + 16, ld_w=pad8(k) + 8, ld_y=ld_y, y_offset=offset)
 
 
+@pytest.mark.parametrize("act", ["none", "gelu"])
+@pytest.mark.parametrize("rows", [5, 16, 17, 32, 33])
+@pytest.mark.parametrize("k,n,ld_y,offset", [(9, 40, 40, 0), (72, 264, 264, 0), (72, 264, 272, 1), (130, 1153, 1160, 0), (130, 1160, 1161, 5),
+                                             (1100, 2600, 2600, 0), (4608, 4600, 4600, 0), (200, 18901, 18904, 0), (200, 19001, 19008, 0)])
+def test_linear_forward_of_rows_that_share_a_weight_tile(rows, k, n, ld_y, offset, act):
+    # a few dozen rows: the weights' features take the place of the rows in the MMAs, split or not
+    run_forward("bf16", rows, k, n, act, ld_y=ld_y, y_offset=offset)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
-@pytest.mark.parametrize("rows,k,n", [(1, 4608, 200), (300, 72, 264), (3000, 72, 1160), (3000, 72, 1161)])
+@pytest.mark.parametrize("rows,k,n", [(16, 72, 264), (40, 1100, 2600), (1, 4608, 200), (300, 72, 264), (3000, 72, 1160), (3000, 72, 1161)])
 def test_linear_forward_adds_in_place(kind, rows, k, n):
     run_forward(kind, rows, k, n, "none", in_place=True, save_z=False)
 

@@ -241,8 +241,13 @@ dsv4v_status gemm(LinearForm form, Operand a, Operand b, int64_t M, int64_t N, i
   if (!query_device(&sms, &err)) return DSV4V_ERR_CUDA;
   const LinearPlan plan = plan_linear(form, M, N, K, sms);
   if (plan.bn == 0) return DSV4V_ERR_UNSUPPORTED;
+  if (plan.swap) {
+    form = LINEAR_FORWARD_SWAPPED;
+    std::swap(a, b);
+    std::swap(M, N);
+  }
   LinearMaps maps;
-  if (!operand_maps(plan, form == LINEAR_WEIGHT_GRAD, form != LINEAR_FORWARD, a, b, M, N, K, &maps.a[0], &maps.b[0])) return DSV4V_ERR_CUDA;
+  if (!operand_maps(plan, form == LINEAR_WEIGHT_GRAD, form == LINEAR_INPUT_GRAD || form == LINEAR_WEIGHT_GRAD, a, b, M, N, K, &maps.a[0], &maps.b[0])) return DSV4V_ERR_CUDA;
   const LinearProduct product{static_cast<int>(M), static_cast<int>(N), e};
   return cuda_status(launch_linear(form, plan, maps, &product, cs, err, s));
 }

@@ -33,6 +33,7 @@ struct ColumnSums {
 
 enum LinearForm {
   LINEAR_FORWARD,      // D[rows, out] = x . W^T: both operands K-major
+  LINEAR_FORWARD_SWAPPED,  // D[out, rows] = W . x^T, of up to 32 rows, stored as y
   LINEAR_INPUT_GRAD,   // dx[rows, in] = dz . W: dz K-major, W MN-major
   LINEAR_WEIGHT_GRAD,  // dW[out, in] = dz^T . x: both MN-major
   LINEAR_BOTH_GRADS,   // dx and dW in one launch
@@ -41,6 +42,7 @@ enum LinearForm {
 // How a launch is cut up; the second entries are dW's of LINEAR_BOTH_GRADS.
 struct LinearPlan {
   int pair = 0, bn = 0, ks = 1;  // CTA pairs; columns of a tile; K splits (cluster size)
+  int swap = 0;                  // the forward as LINEAR_FORWARD_SWAPPED: its M are the features
   int tiles_m[2] = {}, tiles_n[2] = {}, kb_total[2] = {} /* stages */, grid = 0;
   int units = 0;                 // of LINEAR_BOTH_GRADS: CTAs (pairs) of dx
   int a_rows = 0;                // rows of the boxes of a K-major A

@@ -34,6 +34,7 @@ constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kMaxDynSmem = 232448;        // 227 KB per CTA
 constexpr int kBoxBytes = 2048, kBiasBytes = 512;  // per epilogue warp: 32 rows x 64 bytes, and the bias of 4 x 32 columns
 constexpr int kStagingBytes = kEpiWarps * (kBoxBytes + kBiasBytes);
+constexpr int kPartPad = 4;  // puts the rows of a warp's 16-byte accesses to a partial on different banks
 constexpr int kGroupM = 8;                 // row tiles of a raster group
 
 template <int BN, bool PAIR>
@@ -48,9 +49,7 @@ struct Tile {
   static constexpr int SMEM = 1024 + OFF_STAGING + kStagingBytes;
   static constexpr int RING = OFF_BARRIERS;
   static constexpr int TMEM_COLS = 2 * BN <= 128 ? 128 : (2 * BN <= 256 ? 256 : 512);  // two accumulators
-  // Row stride, in floats, of a split's fp32 partial in the ring: 16 bytes off a multiple of 128,
-  // so that the rows of a warp's 16-byte accesses fall on different banks.
-  static constexpr int PART_LD = BN + 4;
+  static constexpr int PART_LD = BN + kPartPad;  // row stride, in floats, of a split's fp32 partial in the ring
   static_assert(PAIR || BM * PART_LD * 4 <= RING, "a partial tile has to fit the ring");
 };
 constexpr int kMaxStages = 16;
@@ -314,19 +313,19 @@ __device__ __forceinline__ void sum_columns(const ColumnSums& cs, int M, int m0)
   cs.out[f] = sum;
 }
 
-// Cluster split-K: this rank's share of a tile.  The tile's 8-column pieces are dealt to the ranks
-// in turn; a piece's partials are all fetched, then summed in rank order.
-template <int BN, bool FWD, int KS>
-__device__ __forceinline__ void finish_pieces(const Job& p, float* part, int slice, int rows, int m0, int n0) {
-  constexpr int PIECES = BN / 8, LD = Tile<BN, false>::PART_LD;
-  const LinearEpilogue& e = p.e;
+// Cluster split-K: this rank's share of a tile of `rows` rows from row m0 and COLS columns from column
+// n0 of N.  The tile's 8-column pieces are dealt to the ranks in turn; a piece's partials are all
+// fetched, then summed in rank order.
+template <int COLS, bool FWD, int KS>
+__device__ __forceinline__ void finish_pieces(const LinearEpilogue& e, float* part, int slice, int rows, int m0, int n0, int N) {
+  constexpr int PIECES = COLS / 8, LD = COLS + kPartPad;
   uint32_t base[KS];
 #pragma unroll
   for (int k = 0; k < KS; ++k) base[k] = mapa_shared(smem_u32(part), static_cast<uint32_t>(k));
   for (int i = (static_cast<int>(threadIdx.x) - 64) * KS + slice; i < rows * PIECES; i += 32 * kEpiWarps * KS) {
     const int lr = i / PIECES, c = (i - lr * PIECES) * 8;
     const int row = m0 + lr, col = n0 + c;
-    if (col >= p.N) continue;
+    if (col >= N) continue;
     const uint32_t at = static_cast<uint32_t>(lr * LD + c) * 4u;
     float4 q[KS][2];
 #pragma unroll
@@ -340,7 +339,7 @@ __device__ __forceinline__ void finish_pieces(const Job& p, float* part, int sli
       v[0] += q[k][0].x, v[1] += q[k][0].y, v[2] += q[k][0].z, v[3] += q[k][0].w;
       v[4] += q[k][1].x, v[5] += q[k][1].y, v[6] += q[k][1].z, v[7] += q[k][1].w;
     }
-    const int n = min(8, p.N - col);
+    const int n = min(8, N - col);
     const bool whole = e.vec_io && n == 8;
     auto put = [&](__nv_bfloat16* dst) {
       if (whole) {
@@ -377,17 +376,22 @@ __device__ __forceinline__ void finish_pieces(const Job& p, float* part, int sli
   }
 }
 
+// The epilogue's warps meet.
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory"); }
+
 // ---------------------------------------------------------------------------- kernel
 // An MN-major operand is loaded as boxes of 64 columns of its stored [K, MN] matrix (atom columns of
 // 64 KPS rows); else K-major, in boxes of 64 columns of its rows.  The forward has bias, activation,
 // residual and the saved pre-activation; the gradients store D as it is.  LINEAR_BOTH_GRADS splits
-// the CTAs between the two gradients.  KS (cluster split-K) is the cluster's size, 1 to 8.
+// the CTAs between the two gradients.  LINEAR_FORWARD_SWAPPED forms D^T = W . x^T for few rows of x, one
+// tile a cluster.  KS (cluster split-K) is the cluster's size, 1 to 8.
 template <int BN, bool PAIR, LinearForm FORM>
 __global__ void __launch_bounds__(kThreads, 1)
     k_linear(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ CUtensorMap tm_b0,
              const __grid_constant__ CUtensorMap tm_a1, const __grid_constant__ CUtensorMap tm_b1,
              const __grid_constant__ Params p, const int ks) {
-  constexpr bool BOTH = FORM == LINEAR_BOTH_GRADS, FWD = FORM == LINEAR_FORWARD, B_MN = !FWD;
+  constexpr bool BOTH = FORM == LINEAR_BOTH_GRADS, SWAP = FORM == LINEAR_FORWARD_SWAPPED, FWD = FORM == LINEAR_FORWARD || SWAP,
+                 B_MN = !FWD;
   using T = Tile<BN, PAIR>;
   constexpr int KPS = T::KPS;
   constexpr int BMT = PAIR ? 2 * BM : BM;
@@ -587,7 +591,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tempty_leader = PAIR ? mapa_shared(smem_u32(tempty), 0) : 0u;
     int acc = 0;
     uint32_t acc_phase = 0;
-    if (PAIR || ks == 1) {
+    if constexpr (SWAP) {
+      // One tile of 128 features a cluster, whose partial is turned round on its way to the ring.
+      constexpr int LD = BM + kPartPad;
+      static_assert(!PAIR && BN * LD * 4 <= T::RING, "the partial has to fit the ring");
+      const int f0 = t_first * BM, rows = job.N;
+      const bool got = mbar_wait(&tfull[0], 0, abort_flag, p.err, kErrTimeoutEpilogue);
+      const bool all_got = __all_sync(0xffffffffu, got);
+      tc_fence_after_sync();
+      float* part = reinterpret_cast<float*>(smem);
+      if (all_got && f0 + quad * 32 < job.M) {
+#pragma unroll 1
+        for (int r0 = 16 * half; r0 < rows; r0 += 32) {
+          uint32_t r[16];
+          tmem_ld16(tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(r0), r);
+          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            asm volatile("" : "+r"(r[j]));
+            if (r0 + j < rows) part[(r0 + j) * LD + quad * 32 + lane] = __uint_as_float(r[j]);
+          }
+        }
+      }
+      __syncwarp();
+      if (ks == 1) epilogue_sync();
+      else cluster_sync();
+      if (ks == 1) finish_pieces<BM, FWD, 1>(e, part, 0, rows, 0, f0, job.M);
+      else finish_pieces<BM, FWD, 2>(e, part, slice, rows, 0, f0, job.M);
+      __syncwarp();
+      if (ks > 1) cluster_sync();  // no CTA leaves while another still reads its partial
+    } else if (PAIR || ks == 1) {
       for (int t = t_first; t < tiles; t += t_step) {
         int mt, nt;
         tile_at(job, t, mt, nt);
@@ -708,9 +741,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       cluster_sync();
-      if (ks == 2) finish_pieces<BN, FWD, 2>(job, part, slice, rows, m0, n0);
-      else if (ks == 4) finish_pieces<BN, FWD, 4>(job, part, slice, rows, m0, n0);
-      else finish_pieces<BN, FWD, 8>(job, part, slice, rows, m0, n0);
+      if (ks == 2) finish_pieces<BN, FWD, 2>(e, part, slice, rows, m0, n0, job.N);
+      else if (ks == 4) finish_pieces<BN, FWD, 4>(e, part, slice, rows, m0, n0, job.N);
+      else finish_pieces<BN, FWD, 8>(e, part, slice, rows, m0, n0, job.N);
       __syncwarp();
       cluster_sync();  // no CTA leaves while another still reads its partial
     }
@@ -740,6 +773,7 @@ cudaError_t launch_tile(const LinearPlan& plan, const LinearMaps& t, const Param
     if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM)) return e;
     if (dev < 64) ready |= uint64_t(1) << dev;
   }
+  static_assert(T::RING == Tile<256, true>::RING, "the plan's number of stages takes one ring size");
   const unsigned span = PAIR ? 2u : static_cast<unsigned>(plan.ks);
   const int second = FORM == LINEAR_BOTH_GRADS ? 1 : 0;
   if (span == 1)
@@ -750,18 +784,23 @@ cudaError_t launch_tile(const LinearPlan& plan, const LinearMaps& t, const Param
 
 template <LinearForm FORM>
 cudaError_t launch_form(const LinearPlan& plan, const LinearMaps& t, const Params& p, cudaStream_t s) {
-  if (plan.pair) {
-    if constexpr (FORM == LINEAR_FORWARD) {
-      if (plan.bn == 160) return launch_tile<160, true, FORM>(plan, t, p, s);
-      if (plan.bn == 192) return launch_tile<192, true, FORM>(plan, t, p, s);
+  if constexpr (FORM == LINEAR_FORWARD_SWAPPED) {
+    if (plan.bn == 16) return launch_tile<16, false, FORM>(plan, t, p, s);
+    if (plan.bn == 32) return launch_tile<32, false, FORM>(plan, t, p, s);
+  } else {
+    if (plan.pair) {
+      if constexpr (FORM == LINEAR_FORWARD) {
+        if (plan.bn == 160) return launch_tile<160, true, FORM>(plan, t, p, s);
+        if (plan.bn == 192) return launch_tile<192, true, FORM>(plan, t, p, s);
+      }
+      if (plan.bn == 128) return launch_tile<128, true, FORM>(plan, t, p, s);
+      if (plan.bn == 256) return launch_tile<256, true, FORM>(plan, t, p, s);
+      return cudaErrorInvalidValue;
     }
-    if (plan.bn == 128) return launch_tile<128, true, FORM>(plan, t, p, s);
-    if (plan.bn == 256) return launch_tile<256, true, FORM>(plan, t, p, s);
-    return cudaErrorInvalidValue;
+    if (plan.bn == 64) return launch_tile<64, false, FORM>(plan, t, p, s);
+    if (plan.bn == 128) return launch_tile<128, false, FORM>(plan, t, p, s);
+    if (plan.bn == 256) return launch_tile<256, false, FORM>(plan, t, p, s);
   }
-  if (plan.bn == 64) return launch_tile<64, false, FORM>(plan, t, p, s);
-  if (plan.bn == 128) return launch_tile<128, false, FORM>(plan, t, p, s);
-  if (plan.bn == 256) return launch_tile<256, false, FORM>(plan, t, p, s);
   return cudaErrorInvalidValue;
 }
 
@@ -919,7 +958,8 @@ namespace {
 // that fewer of the larger ones fit (33 of 4 CTAs and 15 of 8, of 148 SMs).
 constexpr double kStart = 1.8, kPairStart = 0.87, kHandOver = 0.314, kMma = 0.035, kMmaColumn = 0.0011, kBytes = 132e3,
                  kEpilogue = 0.27, kColumn = 0.0207, kPlainColumn = 0.0074, kTile = 0.22, kPairTile = 0.75, kSplit = 1.48,
-                 kSplitColumn = 0.0145, kSplitRank = 0.009;
+                 kSplitColumn = 0.0145, kSplitRank = 0.009, kSwapStage = 0.265, kSwapFinish = 0.25, kSwapSplit = 1.1, kSwapRow = 0.0385;
+constexpr int kSwapRows = 32;  // at 64 columns the tile that holds them is as quick
 
 // The tiles of a product D[M, N] over a contraction of K, and their times.
 struct Tiling {
@@ -981,6 +1021,26 @@ LinearPlan plan_linear(LinearForm form, int64_t M, int64_t N, int64_t K, int sms
         best.grid = static_cast<int>(pair ? 2 * std::min(t.tiles, slots) : (ks > 1 ? t.tiles * ks : std::min(t.tiles, slots)));
       }
     }
+  if (form != LINEAR_FORWARD || M > kSwapRows) return best;
+  // A few rows as columns of D^T = W . x^T: the MMAs of a 128-feature tile then read 128 rows of weights
+  // and 16 or 32 of x, where those of a 64-feature tile read 128 rows of x, existing or not (16 rows of
+  // 256 -> 4608: 3.3 us against 4.3; of 2048 -> 12000: 11.7 against 14.0).
+  LinearPlan p;
+  p.swap = 1;
+  p.bn = M <= 16 ? 16 : 32;
+  p.a_rows = static_cast<int>(std::min<int64_t>(BM, (N + 7) / 8 * 8));
+  const Tiling t(p, form, N, M, K);
+  for (p.ks = 1; p.ks <= 2; ++p.ks) {
+    if (t.tiles * p.ks > sms || (p.ks == 2 && t.kb < 4)) break;
+    const double finish = p.ks == 1 ? kSwapFinish + kSwapRow * p.bn : kSwapSplit + kSwapRow * p.bn;
+    p.us = kStart + kSwapStage * static_cast<double>((t.kb + p.ks - 1) / p.ks) + finish;
+    if (p.us >= best.us) continue;
+    best = p;
+    best.tiles_m[0] = static_cast<int>(t.tm);
+    best.tiles_n[0] = 1;
+    best.kb_total[0] = static_cast<int>(t.kb);
+    best.grid = static_cast<int>(t.tiles) * p.ks;
+  }
   return best;
 }
 
@@ -1039,6 +1099,7 @@ cudaError_t launch_linear(LinearForm form, const LinearPlan& plan, const LinearM
   p.err = err;
   switch (form) {
     case LINEAR_FORWARD: return launch_form<LINEAR_FORWARD>(plan, maps, p, s);
+    case LINEAR_FORWARD_SWAPPED: return launch_form<LINEAR_FORWARD_SWAPPED>(plan, maps, p, s);
     case LINEAR_INPUT_GRAD: return launch_form<LINEAR_INPUT_GRAD>(plan, maps, p, s);
     case LINEAR_WEIGHT_GRAD: return launch_form<LINEAR_WEIGHT_GRAD>(plan, maps, p, s);
     case LINEAR_BOTH_GRADS: return launch_form<LINEAR_BOTH_GRADS>(plan, maps, p, s);
