@@ -250,7 +250,7 @@ def test_linear_backward(rows, k, n, act):
 
 
 @pytest.mark.parametrize("rows,k,n", [(1, 1, 1), (1, 300, 5), (63, 17, 65), (64, 16, 64), (130, 588, 97), (777, 588, 201), (1100, 60, 6),
-                                      (300, 130, 300), (257, 64, 1000)])
+                                      (300, 130, 300), (257, 64, 1000), (5, 60, 1100), (2100, 400, 1001)])
 @pytest.mark.parametrize("act", ["none", "gelu", "silu"])
 def test_linear_backward_fp32(rows, k, n, act):
     run_backward("f32", rows, k, n, act)

@@ -278,13 +278,11 @@ dsv4v_status gemm_grads(const Layer& l, Operand dz, const void* x, const void* w
   return cuda_status(launch_linear(LINEAR_WEIGHT_GRAD, pw, maps, products + 1, cs, err, s));
 }
 
-dsv4v_status gemm_f32(LinearForm form, const void* a, int64_t lda, const void* b, int64_t ldb, int64_t M, int64_t N, int64_t K,
-                      const EpilogueF32& e, cudaStream_t s, const ColumnSums& cs = ColumnSums()) {
+dsv4v_status gemm_f32(LinearForm form, const ProductF32& p, cudaStream_t s, const ColumnSums& cs = ColumnSums()) {
   int sms = 0;
   uint32_t* err = nullptr;
   if (!query_device(&sms, &err)) return DSV4V_ERR_CUDA;
-  return cuda_status(
-      launch_linear_f32(form, static_cast<const float*>(a), lda, static_cast<const float*>(b), ldb, M, N, K, e, cs, err, sms, s));
+  return cuda_status(launch_linear_f32(form, p, cs, err, sms, s));
 }
 
 bool rows16(const void* p, int64_t ld) { return !p || (aligned_to(p, 16) && ld % 8 == 0); }
@@ -294,7 +292,7 @@ dsv4v_status forward(const Layer& l, const void* x, const void* w, const float* 
   if (!l.bf16) {
     const EpilogueF32 e{static_cast<float*>(y), l.ld_y, bias, static_cast<const float*>(residual), l.ld_residual,
                         static_cast<float*>(z), l.ld_z, l.act};
-    return gemm_f32(LINEAR_FORWARD, x, l.ld_x, w, l.ld_w, l.rows, l.n, l.k, e, s);
+    return gemm_f32(LINEAR_FORWARD, ProductF32{static_cast<const float*>(x), l.ld_x, static_cast<const float*>(w), l.ld_w, l.rows, l.n, l.k, e}, s);
   }
   LinearEpilogue e{};
   e.y = static_cast<__nv_bfloat16*>(y);
@@ -359,19 +357,20 @@ dsv4v_status backward(const Layer& l, const void* x, const void* w, const void* 
   const void* dz = write_dz ? static_cast<const void*>(ws + bl.dz) : d_y;
   const int64_t ld_dz = write_dz ? dz_ld(l) : l.ld_y;
   if (!l.bf16) {
-    EpilogueF32 e{};
-    if (dx) {
-      e.y = static_cast<float*>(dx);
-      e.ld_y = l.ld_x;
-      const dsv4v_status st = gemm_f32(LINEAR_INPUT_GRAD, dz, ld_dz, w, l.ld_w, l.rows, l.k, l.n, e, s);
-      if (st != DSV4V_OK) return st;
+    const float* z32 = static_cast<const float*>(dz);
+    ProductF32 px{z32, ld_dz, static_cast<const float*>(w), l.ld_w, l.rows, l.k, l.n, {}};
+    ProductF32 pw{z32, ld_dz, static_cast<const float*>(x), l.ld_x, l.n, l.k, l.rows, {}};
+    px.e.y = static_cast<float*>(dx);
+    px.e.ld_y = l.ld_x;
+    pw.e.y = static_cast<float*>(dw);
+    pw.e.ld_y = l.ld_w;
+    if (dx && dw) {
+      uint32_t* err = nullptr;
+      if (!query_device(nullptr, &err)) return DSV4V_ERR_CUDA;
+      return cuda_status(launch_linear_f32_grads(px, pw, cs, err, sms, s));
     }
-    if (dw) {
-      e.y = static_cast<float*>(dw);
-      e.ld_y = l.ld_w;
-      return gemm_f32(LINEAR_WEIGHT_GRAD, dz, ld_dz, x, l.ld_x, l.n, l.k, l.rows, e, s, cs);
-    }
-    return DSV4V_OK;
+    if (dx) return gemm_f32(LINEAR_INPUT_GRAD, px, s);
+    return dw ? gemm_f32(LINEAR_WEIGHT_GRAD, pw, s, cs) : DSV4V_OK;
   }
   LinearEpilogue ex{}, ew{};
   ex.y = static_cast<__nv_bfloat16*>(dx);

@@ -85,7 +85,19 @@ struct EpilogueF32 {
   int64_t ld_z;
   int act;
 };
-cudaError_t launch_linear_f32(LinearForm form, const float* a, int64_t lda, const float* b, int64_t ldb, int64_t M, int64_t N,
-                              int64_t K, const EpilogueF32& e, const ColumnSums& cs, uint32_t* err, int sms, cudaStream_t s);
+// D[M, N] over a contraction of K.  a is stored [M, K], for the weight gradient [K, M]; b [N, K], for the
+// gradients [K, N].
+struct ProductF32 {
+  const float* a;
+  int64_t lda;
+  const float* b;
+  int64_t ldb;
+  int64_t M, N, K;
+  EpilogueF32 e;
+};
+cudaError_t launch_linear_f32(LinearForm form, const ProductF32& p, const ColumnSums& cs, uint32_t* err, int sms, cudaStream_t s);
+// Both gradients: in one launch where their tiles fit the SMs together, else one after the other.
+cudaError_t launch_linear_f32_grads(const ProductF32& dx, const ProductF32& dw, const ColumnSums& cs, uint32_t* err, int sms,
+                                    cudaStream_t s);
 
 }  // namespace dsv4v

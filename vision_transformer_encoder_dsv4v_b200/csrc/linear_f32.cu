@@ -195,10 +195,13 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err, code));
 }
 
+// One tile of a product, by a cluster of ks CTAs.
 template <bool A_K, bool B_K>
-__global__ void __launch_bounds__(kThreads, 1) k_linear_f32(const float* a, int64_t lda, const float* b, int64_t ldb, int64_t M,
-                                                            int64_t N, int64_t K, const EpilogueF32 e, const ColumnSums cs, uint32_t* err,
-                                                            const int ks) {
+__device__ __forceinline__ void compute_tile(const ProductF32& job, int64_t m_tile, int64_t n_tile, const ColumnSums& cs, uint32_t* err,
+                                             const int ks) {
+  const float *const a = job.a, *const b = job.b;
+  const int64_t lda = job.lda, ldb = job.ldb, M = job.M, N = job.N, K = job.K;
+  const EpilogueF32 e = job.e;  // a copy: its address, which store_column_plain takes, keeps registers free in the loop
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
@@ -236,11 +239,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_f32(const float* a, int6
   grid_dependency_wait();
 
   const int rank = ks > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x / ks) * TM, n0 = static_cast<int64_t>(blockIdx.y) * TN;
+  const int64_t m0 = m_tile * TM, n0 = n_tile * TN;
   const int64_t all_stages = (K + TK - 1) / TK, first = all_stages * rank / ks;
   const int stages = static_cast<int>(all_stages * (rank + 1) / ks - first);  // this rank's
   float* sums = reinterpret_cast<float*>(smem);  // [TM][kSumLd], once the ring is done with
-  if (!A_K && cs.out && blockIdx.y == 0 && rank == 0 && threadIdx.x < TM && m0 + threadIdx.x < M) {
+  if (!A_K && cs.out && n_tile == 0 && rank == 0 && threadIdx.x < TM && m0 + threadIdx.x < M) {
     // the bias gradient of dW's rows, from the strips' sums in order
     float sum = 0.0f;
 #pragma unroll 8
@@ -400,27 +403,57 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_f32(const float* a, int6
 }
 
 template <bool A_K, bool B_K>
-cudaError_t launch(const float* a, int64_t lda, const float* b, int64_t ldb, int64_t M, int64_t N, int64_t K, const EpilogueF32& e,
-                   const ColumnSums& cs, uint32_t* err, int sms, cudaStream_t s) {
-  auto kern = k_linear_f32<A_K, B_K>;
+__global__ void __launch_bounds__(kThreads, 1)
+    k_linear_f32(const __grid_constant__ ProductF32 job, const ColumnSums cs, uint32_t* err, const int ks) {
+  compute_tile<A_K, B_K>(job, blockIdx.x / ks, blockIdx.y, cs, err, ks);
+}
+
+// The tiles of dx, then those of dW: for small layers, whose tiles leave SMs idle in two launches and
+// whose launches are mostly start and end (128 rows, 256 -> 640: 11.3 us, where two launches took 19.8).
+// A rank may have no stage of the shorter contraction; its sums are then zeros.
+__global__ void __launch_bounds__(kThreads, 1)
+    k_linear_f32_grads(const __grid_constant__ ProductF32 dx, const __grid_constant__ ProductF32 dw, const int dx_tiles, const ColumnSums cs,
+                       uint32_t* err, const int ks) {
+  const int t = static_cast<int>(blockIdx.x) / ks;
+  if (t < dx_tiles) {
+    const int n = static_cast<int>((dx.N + TN - 1) / TN);
+    compute_tile<true, false>(dx, t / n, t % n, cs, err, ks);
+  } else {
+    const int n = static_cast<int>((dw.N + TN - 1) / TN);
+    compute_tile<false, false>(dw, (t - dx_tiles) / n, (t - dx_tiles) % n, cs, err, ks);
+  }
+}
+
+int64_t tiles_of(const ProductF32& p) { return (p.M + TM - 1) / TM * ((p.N + TN - 1) / TN); }
+int64_t stages_of(const ProductF32& p) { return (p.K + TK - 1) / TK; }
+
+// The split that leaves no SM a second CTA (15 clusters of eight and 33 of four fit 148 SMs), two
+// stages a rank at least (of the longer contraction, where two products share a launch).
+int split_of(int64_t tiles, int64_t stages, int sms) {
+  return tiles <= sms * 15 / 148 && stages >= 16 ? 8
+         : tiles <= sms * 33 / 148 && stages >= 8 ? 4
+         : tiles * 2 <= sms && stages >= 4        ? 2
+                                                  : 1;
+}
+
+template <auto KERNEL, typename... Params>
+cudaError_t launch(dim3 grid, int ks, cudaStream_t s, const Params&... params) {
   static thread_local uint64_t ready = 0;  // devices on which the shared-memory limit is raised
   int dev = 0;
   if (cudaError_t r = cudaGetDevice(&dev)) return r;
   if (dev >= 64 || !(ready >> dev & 1u)) {
-    if (cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) return r;
+    if (cudaError_t r = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) return r;
     if (dev < 64) ready |= uint64_t(1) << dev;
   }
-  const int64_t tm = (M + TM - 1) / TM, tn = (N + TN - 1) / TN, stages = (K + TK - 1) / TK;
-  // The split that leaves no SM a second CTA (15 clusters of eight and 33 of four fit 148 SMs), two
-  // stages a rank at least.
-  const int64_t tiles = tm * tn;
-  const int ks = tiles <= sms * 15 / 148 && stages >= 16 ? 8
-                 : tiles <= sms * 33 / 148 && stages >= 8 ? 4
-                 : tiles * 2 <= sms && stages >= 4        ? 2
-                                                          : 1;
-  const dim3 grid(static_cast<unsigned>(tm * ks), static_cast<unsigned>(tn));
-  if (ks == 1) return launch_pdl(kern, grid, dim3(kThreads), kSmem, s, a, lda, b, ldb, M, N, K, e, cs, err, 1);
-  return launch_pdl_cluster(kern, grid, dim3(kThreads), kSmem, s, static_cast<unsigned>(ks), a, lda, b, ldb, M, N, K, e, cs, err, ks);
+  if (ks == 1) return launch_pdl(KERNEL, grid, dim3(kThreads), kSmem, s, params...);
+  return launch_pdl_cluster(KERNEL, grid, dim3(kThreads), kSmem, s, static_cast<unsigned>(ks), params...);
+}
+
+template <bool A_K, bool B_K>
+cudaError_t launch_product(const ProductF32& p, const ColumnSums& cs, uint32_t* err, int sms, cudaStream_t s) {
+  const int ks = split_of(tiles_of(p), stages_of(p), sms);
+  const dim3 grid(static_cast<unsigned>((p.M + TM - 1) / TM * ks), static_cast<unsigned>((p.N + TN - 1) / TN));
+  return launch<k_linear_f32<A_K, B_K>>(grid, ks, s, p, cs, err, ks);
 }
 
 // ---------------------------------------------------------------------------- a few rows
@@ -483,29 +516,38 @@ __global__ void __launch_bounds__(kFewThreads) k_linear_few_f32(const float* x, 
 }
 
 template <int R>
-cudaError_t launch_few(const float* x, int64_t ld_x, const float* w, int64_t ld_w, int64_t rows, int64_t N, int64_t K,
-                       const EpilogueF32& e, int sms, cudaStream_t s) {
+cudaError_t launch_few(const ProductF32& p, int sms, cudaStream_t s) {
   const int64_t per = kFewThreads / 32;
-  const int grid = static_cast<int>(std::min<int64_t>((N + per - 1) / per, sms * 4));
-  const bool vec = (reinterpret_cast<uintptr_t>(w) & 15) == 0 && ld_w % 4 == 0;
-  return launch_pdl(k_linear_few_f32<R>, dim3(grid), dim3(kFewThreads), static_cast<size_t>(R) * ((K + 3) / 4 * 16), s, x, ld_x, w, ld_w,
-                    static_cast<int>(rows), static_cast<int>(N), static_cast<int>(K), vec, e);
+  const int grid = static_cast<int>(std::min<int64_t>((p.N + per - 1) / per, sms * 4));
+  const bool vec = (reinterpret_cast<uintptr_t>(p.b) & 15) == 0 && p.ldb % 4 == 0;
+  return launch_pdl(k_linear_few_f32<R>, dim3(grid), dim3(kFewThreads), static_cast<size_t>(R) * ((p.K + 3) / 4 * 16), s, p.a, p.lda, p.b,
+                    p.ldb, static_cast<int>(p.M), static_cast<int>(p.N), static_cast<int>(p.K), vec, p.e);
 }
 
 }  // namespace
 
-cudaError_t launch_linear_f32(LinearForm form, const float* a, int64_t lda, const float* b, int64_t ldb, int64_t M, int64_t N,
-                              int64_t K, const EpilogueF32& e, const ColumnSums& cs, uint32_t* err, int sms, cudaStream_t s) {
-  if (form == LINEAR_FORWARD && M <= 4 && (M <= 2 ? M : 4) * ((K + 3) / 4 * 16) <= kFewSmem)
-    return M == 1   ? launch_few<1>(a, lda, b, ldb, M, N, K, e, sms, s)
-           : M == 2 ? launch_few<2>(a, lda, b, ldb, M, N, K, e, sms, s)
-                    : launch_few<4>(a, lda, b, ldb, M, N, K, e, sms, s);
+cudaError_t launch_linear_f32(LinearForm form, const ProductF32& p, const ColumnSums& cs, uint32_t* err, int sms, cudaStream_t s) {
+  if (form == LINEAR_FORWARD && p.M <= 4 && (p.M <= 2 ? p.M : 4) * ((p.K + 3) / 4 * 16) <= kFewSmem)
+    return p.M == 1   ? launch_few<1>(p, sms, s)
+           : p.M == 2 ? launch_few<2>(p, sms, s)
+                      : launch_few<4>(p, sms, s);
   switch (form) {
-    case LINEAR_FORWARD: return launch<true, true>(a, lda, b, ldb, M, N, K, e, cs, err, sms, s);
-    case LINEAR_INPUT_GRAD: return launch<true, false>(a, lda, b, ldb, M, N, K, e, cs, err, sms, s);
-    case LINEAR_WEIGHT_GRAD: return launch<false, false>(a, lda, b, ldb, M, N, K, e, cs, err, sms, s);
+    case LINEAR_FORWARD: return launch_product<true, true>(p, cs, err, sms, s);
+    case LINEAR_INPUT_GRAD: return launch_product<true, false>(p, cs, err, sms, s);
+    case LINEAR_WEIGHT_GRAD: return launch_product<false, false>(p, cs, err, sms, s);
+    default: return cudaErrorInvalidValue;
   }
-  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_linear_f32_grads(const ProductF32& dx, const ProductF32& dw, const ColumnSums& cs, uint32_t* err, int sms,
+                                    cudaStream_t s) {
+  const int64_t tiles = tiles_of(dx) + tiles_of(dw);
+  if (tiles > sms) {
+    if (cudaError_t r = launch_product<true, false>(dx, ColumnSums(), err, sms, s)) return r;
+    return launch_product<false, false>(dw, cs, err, sms, s);
+  }
+  const int ks = split_of(tiles, std::max(stages_of(dx), stages_of(dw)), sms);
+  return launch<k_linear_f32_grads>(dim3(static_cast<unsigned>(tiles * ks)), ks, s, dx, dw, static_cast<int>(tiles_of(dx)), cs, err, ks);
 }
 
 }  // namespace dsv4v
