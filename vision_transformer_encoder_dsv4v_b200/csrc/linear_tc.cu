@@ -956,6 +956,8 @@ namespace {
 // worst.  A stage takes the longest of its hand-over, its MMAs and its bytes into the SM; an
 // epilogue runs under the next tile's stages where there is one; clusters stay inside a GPC, so
 // that fewer of the larger ones fit (33 of 4 CTAs and 15 of 8, of 148 SMs).
+// The pairs of 160 columns, which came after the fit, take the same constants; the swapped product has
+// its own, from 48 shapes of 3 to 64 rows.
 constexpr double kStart = 1.8, kPairStart = 0.87, kHandOver = 0.314, kMma = 0.035, kMmaColumn = 0.0011, kBytes = 132e3,
                  kEpilogue = 0.27, kColumn = 0.0207, kPlainColumn = 0.0074, kTile = 0.22, kPairTile = 0.75, kSplit = 1.48,
                  kSplitColumn = 0.0145, kSplitRank = 0.009, kSwapStage = 0.265, kSwapFinish = 0.25, kSwapSplit = 1.1, kSwapRow = 0.0385;
