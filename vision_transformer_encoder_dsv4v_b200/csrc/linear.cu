@@ -1,6 +1,7 @@
 // Entry points of the Linear layer (forward and backward) and the kernels around its products: the
 // gradient of the activation, with the bias gradient's sums.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -77,10 +78,13 @@ __device__ __forceinline__ void put8(float* p, const float (&v)[8]) {
 constexpr int kDzCols = 256;  // columns of a CTA: 32 threads of 8, by 8 rows at a time
 
 // One pass over dy (and z): writes dz where it is wanted and, per strip of rows, the column sums of
-// the unrounded dz, whose strips k_column_sums adds in order.  HBM bounds it.
-template <class T, int ACT>
-__global__ void __launch_bounds__(256) k_linear_dz(const T* dy, int64_t ld_dy, const T* z, int64_t ld_z, T* dz, int64_t ld_dz,
-                                                   float* sums, int64_t rows, int n, int64_t strip, bool vec) {
+// the unrounded dz, whose strips k_column_sums adds in order.  HBM bounds it (8192 x 4096 bf16, dy and z
+// read: 25 us, 5.3 TB/s, with four CTAs an SM of two rows in flight a thread; 34 us with two CTAs of
+// four).  VEC: rows are 16-byte aligned.
+template <class T, int ACT, bool VEC>
+__global__ void __launch_bounds__(256, VEC ? (sizeof(T) == 2 ? 4 : 2) : 1)
+    k_linear_dz(const T* dy, int64_t ld_dy, const T* z, int64_t ld_z, T* dz, int64_t ld_dz, float* sums, int64_t rows, int n,
+                int64_t strip) {
   launch_dependents();
   grid_dependency_wait();
   __shared__ float s[8][kDzCols + 8];
@@ -100,23 +104,26 @@ __global__ void __launch_bounds__(256) k_linear_dz(const T* dy, int64_t ld_dy, c
       for (int j = 0; j < 8; ++j) acc[j] += g[j];
     };
     int64_t r = r0 + ry;
-    if (vec && cnt == 8) {
-      constexpr int U = 4;  // rows in flight
-      for (; r + 8 * (U - 1) < r1; r += 8 * U) {
-        Eight<T> qg[U], qv[U];
+    if (VEC && cnt == 8) {
+      constexpr int U = sizeof(T) == 2 ? 2 : 4;  // rows in flight
+      auto batch = [&](auto count) {
+        constexpr int C = decltype(count)::value;
+        Eight<T> qg[C], qv[C];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
+        for (int u = 0; u < C; ++u) {
           qg[u].load(dy + (r + 8 * u) * ld_dy + col);
           if constexpr (ACT != DSV4V_ACT_NONE) qv[u].load(z + (r + 8 * u) * ld_z + col);
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
+        for (int u = 0; u < C; ++u) {
           float g[8], v[8] = {};
           qg[u].values(g);
           if constexpr (ACT != DSV4V_ACT_NONE) qv[u].values(v);
           finish(r + 8 * u, g, v);
         }
-      }
+      };
+      for (; r + 8 * (U - 1) < r1; r += 8 * U) batch(std::integral_constant<int, U>());
+      for (; r < r1; r += 8) batch(std::integral_constant<int, 1>());
     }
     for (; r < r1; r += 8) {
       float g[8], v[8] = {};
@@ -201,10 +208,10 @@ dsv4v_status check_layer(const dsv4v_linear* l, Layer& o) {
 
 int64_t dz_ld(const Layer& l) { return (l.n + 7) / 8 * 8; }
 
-// Strips of rows of the dz pass: about four CTAs an SM, at least 32 rows each.
+// Strips of rows of the dz pass: about four CTAs an SM, at least 16 rows each.
 int dz_strips(const Layer& l, int sms) {
   const int64_t across = (l.n + kDzCols - 1) / kDzCols;
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((l.rows + 31) / 32, 4ll * sms / across)));
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((l.rows + 15) / 16, 4ll * sms / across)));
 }
 
 struct BackwardLayout {
@@ -313,14 +320,19 @@ dsv4v_status forward(const Layer& l, const void* x, const void* w, const float* 
   return gemm(LINEAR_FORWARD, Operand{x, l.ld_x}, Operand{w, l.ld_w}, l.rows, l.n, l.k, e, s);
 }
 
+template <class T, int ACT, bool VEC>
+cudaError_t launch_dz_vec(const Layer& l, const void* d_y, const void* z, void* dz, float* sums, int strips, cudaStream_t s) {
+  const int64_t strip = (l.rows + strips - 1) / strips;
+  return launch_pdl(k_linear_dz<T, ACT, VEC>, dim3(static_cast<unsigned>((l.n + kDzCols - 1) / kDzCols), static_cast<unsigned>(strips)),
+                    dim3(256), 0, s, static_cast<const T*>(d_y), l.ld_y, static_cast<const T*>(z), l.ld_z, static_cast<T*>(dz),
+                    dz_ld(l), sums, l.rows, static_cast<int>(l.n), strip);
+}
+
 template <class T, int ACT>
 cudaError_t launch_dz_act(const Layer& l, const void* d_y, const void* z, void* dz, float* sums, int strips, cudaStream_t s) {
-  const int64_t strip = (l.rows + strips - 1) / strips;
   const bool vec = aligned_to(d_y, 16) && l.ld_y * sizeof(T) % 16 == 0 &&
                    (ACT == DSV4V_ACT_NONE || (aligned_to(z, 16) && l.ld_z * sizeof(T) % 16 == 0));
-  return launch_pdl(k_linear_dz<T, ACT>, dim3(static_cast<unsigned>((l.n + kDzCols - 1) / kDzCols), static_cast<unsigned>(strips)),
-                    dim3(256), 0, s, static_cast<const T*>(d_y), l.ld_y, static_cast<const T*>(z), l.ld_z, static_cast<T*>(dz),
-                    dz_ld(l), sums, l.rows, static_cast<int>(l.n), strip, vec);
+  return vec ? launch_dz_vec<T, ACT, true>(l, d_y, z, dz, sums, strips, s) : launch_dz_vec<T, ACT, false>(l, d_y, z, dz, sums, strips, s);
 }
 
 template <class T>
