@@ -103,22 +103,21 @@ struct NormTable {
 };
 constexpr int kNormCap = NormTable<kParamBytes>::CAP;
 
-// Sum of squares of N values.  fp32 (relative error of a few 2^-24, which the outer fp64 sum
-// averages out) unless the squares leave fp32's range, which a second look in fp64 covers: the
-// norm holds for every finite gradient.
-template <int N>
-__device__ __forceinline__ double squares(const float (&v)[N]) {
+// Sum of squares of eight values.  fp32 (eight roundings, at most 8 x 2^-24 of the sum however the
+// values are made) unless the squares leave fp32's range, which a second look in fp64 covers: the norm
+// holds for every finite gradient.
+__device__ __forceinline__ double squares(const float (&v)[8]) {
   float s = 0.0f;
 #pragma unroll
-  for (int j = 0; j < N; ++j) s = fmaf(v[j], v[j], s);
+  for (int j = 0; j < 8; ++j) s = fmaf(v[j], v[j], s);
   if (s > 1e-30f && s < 1e37f) return static_cast<double>(s);
   double d = 0.0;
 #pragma unroll
-  for (int j = 0; j < N; ++j) d = fma(static_cast<double>(v[j]), static_cast<double>(v[j]), d);
+  for (int j = 0; j < 8; ++j) d = fma(static_cast<double>(v[j]), static_cast<double>(v[j]), d);
   return d;
 }
 
-__device__ __forceinline__ void unpack8(const uint4& q, float* v) {
+__device__ __forceinline__ void unpack8(const uint4& q, float (&v)[8]) {
   v[0] = bf16_lo(q.x), v[1] = bf16_hi(q.x), v[2] = bf16_lo(q.y), v[3] = bf16_hi(q.y);
   v[4] = bf16_lo(q.z), v[5] = bf16_hi(q.z), v[6] = bf16_lo(q.w), v[7] = bf16_hi(q.w);
 }
@@ -138,7 +137,8 @@ __device__ __forceinline__ double block_sum(double v) {
 }
 
 // 64 bytes of a thread are in flight at a time for bf16 and 128 for fp32, 64 to 128 KB an SM, which
-// is what hides HBM's latency.
+// is what hides HBM's latency.  A thread sums the same elements in the same order whether a chunk is
+// whole, ragged or unaligned, so the norm does not depend on where the tensors lie.
 template <int BYTES>
 __global__ void __launch_bounds__(kThreads, 4) k_grad_norm(const __grid_constant__ NormTable<BYTES> t) {
   launch_dependents();
@@ -157,21 +157,22 @@ __global__ void __launch_bounds__(kThreads, 4) k_grad_norm(const __grid_constant
 #pragma unroll
         for (int u = 0; u < 4; ++u) q[u] = p[u * kThreads];
 #pragma unroll
-        for (int u = 0; u < 4; u += 2) {
-          float v[16];
+        for (int u = 0; u < 4; ++u) {
+          float v[8];
           unpack8(q[u], v);
-          unpack8(q[u + 1], v + 8);
           acc += squares(v);
         }
       } else {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(e.data) + i0) + threadIdx.x;
+        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(e.data) + i0) + 2 * threadIdx.x;
         float4 q[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) q[u] = p[u * kThreads];
+        for (int u = 0; u < 4; ++u) {
+          q[2 * u] = p[2 * u * kThreads];
+          q[2 * u + 1] = p[2 * u * kThreads + 1];
+        }
 #pragma unroll
-        for (int u = 0; u < 8; u += 4) {
-          const float v[16] = {q[u].x, q[u].y, q[u].z, q[u].w, q[u + 1].x, q[u + 1].y, q[u + 1].z, q[u + 1].w,
-                               q[u + 2].x, q[u + 2].y, q[u + 2].z, q[u + 2].w, q[u + 3].x, q[u + 3].y, q[u + 3].z, q[u + 3].w};
+        for (int u = 0; u < 8; u += 2) {
+          const float v[8] = {q[u].x, q[u].y, q[u].z, q[u].w, q[u + 1].x, q[u + 1].y, q[u + 1].z, q[u + 1].w};
           acc += squares(v);
         }
       }
