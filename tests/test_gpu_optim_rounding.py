@@ -59,3 +59,27 @@ def test_grad_norm_does_not_depend_on_the_address(dtype, piece, runs, n):
     g = ones_among_small(n, piece, runs, dtype)
     got = [norm_of([at_offset(g, offset)]) for offset in range(8)]
     assert all(torch.equal(got[0], x) for x in got[1:])
+
+
+# ---------------------------------------------------------------------------------------------- AdamW
+@pytest.mark.parametrize("decay", [1e-8, 3e-8, 1e-7, 1e-6])
+@pytest.mark.parametrize("on_device", [False, True])
+def test_adamw_takes_a_small_decay_on_average(decay, on_device):
+    # weights from 1 to 2, whose step (2 u) is above lr weight_decay, and updates of a few such steps: each result's
+    # rounding is even over a step, so the mean over n weights is off by 2 u / sqrt(12 n) times a few, beside 20 u of
+    # the update and of the decay
+    n, lr, step = 1 << 20, 2.0 ** -20, 1000
+    gen = torch.Generator().manual_seed(0)
+    uniform = lambda lo, hi: (lo + (hi - lo) * torch.rand(n, generator=gen)).cuda()  # noqa: E731
+    p, m, v = uniform(1, 2), uniform(-0.1, 0.1), uniform(1e-3, 1e-2)
+    g = torch.randn(n, generator=gen).cuda()
+    want, _, _ = O.adamw(np64(p), np64(g), np64(m), np64(v), step, lr, decay=decay / lr)
+    size = np.abs(want - np64(p)).max()
+    table = A.AdamwTable([dict(param=p, grad=g, exp_avg=m, exp_avg_sq=v, weight_decay=decay / lr)])
+    if on_device:
+        count, rate = torch.tensor(step - 1, device="cuda"), torch.tensor(lr, device="cuda")
+        A.dsv4v_adamw_step(A.make_adamw(1.0), table, lr_dev=rate, step_dev=count)
+    else:
+        A.dsv4v_adamw_step(A.make_adamw(lr, step=step), table)
+    mean = (np64(p) - want).mean()
+    assert abs(mean) <= 6 * 2 * U / np.sqrt(12 * n) + 20 * U * size

@@ -332,12 +332,14 @@ struct AdamScalars {
 
 // One AdamW step of the 8 elements that a thread holds:
 //   g' = g min(1, max_norm / norm);  m = b1 m + (1 - b1) g';  v = b2 v + (1 - b2) g'^2
-//   p = p (1 - lr decay) - (lr / (1 - b1^t)) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+//   p = p - (lr decay p + (lr / (1 - b1^t)) m / (sqrt(v) / sqrt(1 - b2^t) + eps))
+// The decay joins the update before p is rounded: as a factor 1 - lr decay it would come in steps of
+// 2^-24, and not at all below 3e-8, where the ends of a schedule take it.
 // m and v take each product and sum rounded by itself (no contraction): a block's scale then
 // depends on the formula alone, not on how a compiler fuses it.  The update's root and quotient
 // come from the MUFU pipe, off by 2^-23 of the update, which leaves the 8-bit step's 60 instructions an
 // element within HBM's time.
-__device__ __forceinline__ void adam8(const AdamScalars& a, float keep, const float (&g)[8], float (&p)[8], float (&m)[8],
+__device__ __forceinline__ void adam8(const AdamScalars& a, float decay, const float (&g)[8], float (&p)[8], float (&m)[8],
                                       float (&v)[8], float (&root)[8]) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -345,7 +347,7 @@ __device__ __forceinline__ void adam8(const AdamScalars& a, float keep, const fl
     m[j] = __fadd_rn(__fmul_rn(m[j], a.b1), __fmul_rn(gj, a.c1));
     v[j] = __fadd_rn(__fmul_rn(v[j], a.b2), __fmul_rn(__fmul_rn(gj, gj), a.c2));
     root[j] = sqrt_approx(v[j]);
-    p[j] = fmaf(p[j], keep, -a.step_size * m[j] * rcp_approx(fmaf(root[j], a.inv_root, a.eps)));
+    p[j] -= fmaf(decay, p[j], a.step_size * m[j] * rcp_approx(fmaf(root[j], a.inv_root, a.eps)));
   }
 }
 
@@ -386,7 +388,7 @@ __device__ __forceinline__ void adam_codes(const float (&m)[8], const float (&v)
 // The usual case, 8 elements that exist behind aligned pointers.  The types are template
 // parameters, so that all loads are issued before the first of them is waited for.
 template <uint32_t KIND>
-__device__ __forceinline__ void adam_whole(const AdamEntry& e, const AdamScalars& a, float keep, int64_t i, int lane) {
+__device__ __forceinline__ void adam_whole(const AdamEntry& e, const AdamScalars& a, float decay, int64_t i, int lane) {
   constexpr bool PB = KIND & kParamBf16, GB = KIND & kGradBf16, S8 = KIND & kState8, MASTER = KIND & kMaster;
   float g[8], p[8], m[8], v[8], root[8];
   uint2 mc, vc;
@@ -407,7 +409,7 @@ __device__ __forceinline__ void adam_whole(const AdamEntry& e, const AdamScalars
     load8(e.m, false, true, i, 8, m);
     load8(e.v, false, true, i, 8, v);
   }
-  adam8(a, keep, g, p, m, v, root);
+  adam8(a, decay, g, p, m, v, root);
   store8(e.param, PB, true, i, 8, p);
   if constexpr (MASTER) store8(e.master, false, true, i, 8, p);
   if constexpr (S8) {
@@ -426,7 +428,7 @@ __device__ __forceinline__ void adam_whole(const AdamEntry& e, const AdamScalars
 
 // A tensor's ragged end, and tensors that are not aligned: any types, `cnt` elements (at most 8; for
 // the lanes behind the end, 0 or less).
-__device__ __noinline__ void adam_ragged(const AdamEntry& e, const AdamScalars& a, float keep, int64_t i, int cnt, int lane) {
+__device__ __noinline__ void adam_ragged(const AdamEntry& e, const AdamScalars& a, float decay, int64_t i, int cnt, int lane) {
   const bool vec = e.flags & kVector, s8 = e.flags & kState8, pb = e.flags & kParamBf16;
   const int64_t block = (i - lane * 8) / kStateBlock;
   float g[8], p[8], m[8], v[8], root[8];
@@ -442,7 +444,7 @@ __device__ __noinline__ void adam_ragged(const AdamEntry& e, const AdamScalars& 
     load8(e.m, false, vec, i, cnt, m);
     load8(e.v, false, vec, i, cnt, v);
   }
-  adam8(a, keep, g, p, m, v, root);
+  adam8(a, decay, g, p, m, v, root);
   store8(e.param, pb, vec, i, cnt, p);
   if (e.master) store8(e.master, false, vec, i, cnt, p);
   if (s8) {
@@ -492,26 +494,26 @@ __global__ void __launch_bounds__(kThreads, 4) k_adamw(const __grid_constant__ A
 
   const uint32_t c = blockIdx.x;
   const AdamEntry& e = t.e[tensor_of(t, c, 0)];
-  const float keep = static_cast<float>(1.0 - lr * e.decay);
+  const float decay = static_cast<float>(lr * e.decay);
   const int64_t i = static_cast<int64_t>(c - e.chunk0) * kAdamChunk + threadIdx.x * 8;
   const int64_t end = i - lane * 8 + 256;  // of the warp's elements
   if (end <= e.n && (e.flags & kVector)) {
     switch (e.flags & 15u) {
-      case 0: adam_whole<0>(e, a, keep, i, lane); break;
-      case kParamBf16: adam_whole<kParamBf16>(e, a, keep, i, lane); break;
-      case kGradBf16: adam_whole<kGradBf16>(e, a, keep, i, lane); break;
-      case kParamBf16 | kGradBf16: adam_whole<kParamBf16 | kGradBf16>(e, a, keep, i, lane); break;
-      case kState8: adam_whole<kState8>(e, a, keep, i, lane); break;
-      case kState8 | kParamBf16: adam_whole<kState8 | kParamBf16>(e, a, keep, i, lane); break;
-      case kState8 | kGradBf16: adam_whole<kState8 | kGradBf16>(e, a, keep, i, lane); break;
-      case kState8 | kParamBf16 | kGradBf16: adam_whole<kState8 | kParamBf16 | kGradBf16>(e, a, keep, i, lane); break;
-      case kMaster | kParamBf16: adam_whole<kMaster | kParamBf16>(e, a, keep, i, lane); break;
-      case kMaster | kParamBf16 | kGradBf16: adam_whole<kMaster | kParamBf16 | kGradBf16>(e, a, keep, i, lane); break;
-      case kMaster | kState8 | kParamBf16: adam_whole<kMaster | kState8 | kParamBf16>(e, a, keep, i, lane); break;
-      default: adam_whole<kMaster | kState8 | kParamBf16 | kGradBf16>(e, a, keep, i, lane); break;
+      case 0: adam_whole<0>(e, a, decay, i, lane); break;
+      case kParamBf16: adam_whole<kParamBf16>(e, a, decay, i, lane); break;
+      case kGradBf16: adam_whole<kGradBf16>(e, a, decay, i, lane); break;
+      case kParamBf16 | kGradBf16: adam_whole<kParamBf16 | kGradBf16>(e, a, decay, i, lane); break;
+      case kState8: adam_whole<kState8>(e, a, decay, i, lane); break;
+      case kState8 | kParamBf16: adam_whole<kState8 | kParamBf16>(e, a, decay, i, lane); break;
+      case kState8 | kGradBf16: adam_whole<kState8 | kGradBf16>(e, a, decay, i, lane); break;
+      case kState8 | kParamBf16 | kGradBf16: adam_whole<kState8 | kParamBf16 | kGradBf16>(e, a, decay, i, lane); break;
+      case kMaster | kParamBf16: adam_whole<kMaster | kParamBf16>(e, a, decay, i, lane); break;
+      case kMaster | kParamBf16 | kGradBf16: adam_whole<kMaster | kParamBf16 | kGradBf16>(e, a, decay, i, lane); break;
+      case kMaster | kState8 | kParamBf16: adam_whole<kMaster | kState8 | kParamBf16>(e, a, decay, i, lane); break;
+      default: adam_whole<kMaster | kState8 | kParamBf16 | kGradBf16>(e, a, decay, i, lane); break;
     }
   } else if (end - 256 < e.n) {
-    adam_ragged(e, a, keep, i, static_cast<int>(min(int64_t(8), e.n - i)), lane);
+    adam_ragged(e, a, decay, i, static_cast<int>(min(int64_t(8), e.n - i)), lane);
   }
 }
 
