@@ -548,6 +548,19 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 // The two bf16 of a packed pair as a packed fp32 pair.
 __device__ __forceinline__ uint64_t bf16x2_f2(uint32_t v) { return pk2(bf16_lo(v), bf16_hi(v)); }
 
+// Launches `kern` behind everything ahead of it on the stream.  The status is this launch's own (an
+// execution configuration in <<<>>> leaves it to cudaGetLastError, which also returns what an earlier call
+// of the thread left there).
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_plain(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
 // Launches `kern` with programmatic stream serialization (dependent launch) allowed: the kernel
 // may begin while the previous kernel on the stream is still running, and must call
 // grid_dependency_wait() before touching that kernel's data.

@@ -686,8 +686,7 @@ dsv4v_status dsv4v_adamw_step(const dsv4v_adamw_config* cfg, const dsv4v_adamw_t
                                                      : launch_adamw<kParamBytes>(a, tensors, i, n_tensors, sms, s);
     if (i < 0) return DSV4V_ERR_CUDA;
   }
-  k_adamw_end<<<1, 1, 0, s>>>(step_dev, grad_norm);
-  return cudaGetLastError() == cudaSuccess ? DSV4V_OK : DSV4V_ERR_CUDA;
+  return launch_plain(k_adamw_end, dim3(1), dim3(1), 0, s, step_dev, grad_norm) == cudaSuccess ? DSV4V_OK : DSV4V_ERR_CUDA;
 }
 
 }  // extern "C"

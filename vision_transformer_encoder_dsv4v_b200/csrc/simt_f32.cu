@@ -139,37 +139,33 @@ cudaError_t launch_gemm_f32(int epi, const float* a, const float* b, const float
   if (M == 0) return cudaSuccess;
   dim3 grid((n_out + T - 1) / T, (M + T - 1) / T);
   switch (epi) {
-    case EPI_STORE: k_gemm_f32<EPI_STORE><<<grid, 256, 0, s>>>(a, b, b2, out, resid, M, n_out, K, bias); break;
-    case EPI_RESID: k_gemm_f32<EPI_RESID><<<grid, 256, 0, s>>>(a, b, b2, out, resid, M, n_out, K, nullptr); break;
-    case EPI_SWIGLU: k_gemm_f32<EPI_SWIGLU><<<grid, 256, 0, s>>>(a, b, b2, out, resid, M, n_out, K, nullptr); break;
-    case EPI_GELU: k_gemm_f32<EPI_GELU><<<grid, 256, 0, s>>>(a, b, b2, out, resid, M, n_out, K, bias); break;
-    default: return cudaErrorInvalidValue;
+    case EPI_STORE: return launch_plain(k_gemm_f32<EPI_STORE>, grid, dim3(256), 0, s, a, b, b2, out, resid, M, n_out, K, bias);
+    case EPI_RESID: return launch_plain(k_gemm_f32<EPI_RESID>, grid, dim3(256), 0, s, a, b, b2, out, resid, M, n_out, K, nullptr);
+    case EPI_SWIGLU: return launch_plain(k_gemm_f32<EPI_SWIGLU>, grid, dim3(256), 0, s, a, b, b2, out, resid, M, n_out, K, nullptr);
+    case EPI_GELU: return launch_plain(k_gemm_f32<EPI_GELU>, grid, dim3(256), 0, s, a, b, b2, out, resid, M, n_out, K, bias);
   }
-  return cudaGetLastError();
+  return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_rope_apply_f32(float* qkv, const float* cos, const float* sin, int64_t P, int d, int n_heads,
                                   cudaStream_t s) {
   const int64_t n = P * d;  // 2 sections x n_heads x hd/2 pairs = d
   if (n == 0) return cudaSuccess;
-  k_rope_apply_f32<<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(qkv, cos, sin, P, d, n_heads);
-  return cudaGetLastError();
+  return launch_plain(k_rope_apply_f32, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, s, qkv, cos, sin, P, d, n_heads);
 }
 
 cudaError_t launch_attention_f32(const float* qkv, float* out, const int32_t* cu_dev, int n_images, int64_t P,
                                  int d, int n_heads, cudaStream_t s) {
   const int64_t n = P * n_heads;
   if (n == 0) return cudaSuccess;
-  k_attention_f32<<<static_cast<unsigned>((n + 127) / 128), 128, 0, s>>>(qkv, out, cu_dev, n_images, P, d, n_heads);
-  return cudaGetLastError();
+  return launch_plain(k_attention_f32, dim3(static_cast<unsigned>((n + 127) / 128)), dim3(128), 0, s, qkv, out, cu_dev, n_images, P, d, n_heads);
 }
 
 cudaError_t launch_gather_f32(const float* x, const int32_t* src, float* merged, int64_t n_tokens, int r2, int d,
                               cudaStream_t s) {
   const int64_t n = n_tokens * r2 * d;
   if (n == 0) return cudaSuccess;
-  k_gather_f32<<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(x, src, merged, n_tokens, r2, d);
-  return cudaGetLastError();
+  return launch_plain(k_gather_f32, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, s, x, src, merged, n_tokens, r2, d);
 }
 
 }  // namespace dsv4v

@@ -279,8 +279,7 @@ cudaError_t launch_rmsnorm(bool bf16, const void* x, const float* w, void* y, in
   const unsigned blocks = static_cast<unsigned>((rows + warps - 1) / warps);
   if (bf16)
     return launch_pdl(k_rmsnorm<true>, dim3(blocks), dim3(warps * 32), 0, s, x, w, y, rows, d, eps, zero_ptr, zero_n);
-  k_rmsnorm<false><<<blocks, warps * 32, 0, s>>>(x, w, y, rows, d, eps, zero_ptr, zero_n);
-  return cudaGetLastError();
+  return launch_plain(k_rmsnorm<false>, dim3(blocks), dim3(warps * 32), 0, s, x, w, y, rows, d, eps, zero_ptr, zero_n);
 }
 
 cudaError_t launch_norm_prep(const void* x, const float* w, void* xw, float* ss, int parts, int64_t rows, int d,
@@ -328,8 +327,7 @@ cudaError_t launch_zero_counters(int* ptr, int n, cudaStream_t s) {
 }
 
 cudaError_t launch_selftest_wait(uint64_t limit_ns, uint32_t* err, cudaStream_t s) {
-  k_selftest_wait<<<1, 32, 0, s>>>(limit_ns, err);
-  return cudaGetLastError();
+  return launch_plain(k_selftest_wait, dim3(1), dim3(32), 0, s, limit_ns, err);
 }
 
 }  // namespace dsv4v
