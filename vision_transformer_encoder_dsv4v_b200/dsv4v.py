@@ -389,7 +389,14 @@ def dsv4v_backward_workspace_size(cfg, batch) -> int:
 
 
 def _ws(workspace):
-    return _ptr(workspace), workspace.numel() if workspace is not None else 0
+    """The address and the bytes of a workspace, which has to lie on the current device."""
+    if workspace is None:
+        return None, 0
+    if not workspace.is_cuda or workspace.get_device() != _device_index():
+        raise ValueError(f"workspace is on {workspace.device}, the current device is cuda:{_device_index()}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace is not contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def dsv4v_attention_backward(cfg, batch, qkv, out, d_out, dqkv, workspace, stream=None):
