@@ -427,7 +427,7 @@ dsv4v_status dsv4v_linear_forward(const dsv4v_linear* layer, const void* x, cons
   if (!x || !w || !y || !aligned_to(x, in) || !aligned_to(w, in) || !aligned_to(y, l.es) || (bias && !aligned_to(bias, 16)) ||
       (residual && !aligned_to(residual, l.es)) || (z && !aligned_to(z, l.es)))
     return DSV4V_ERR_INVALID_ARG;
-  if (y == x || z == x || z == y || (z && z == residual) || (residual == y && l.ld_residual != l.ld_y)) return DSV4V_ERR_INVALID_ARG;
+  if (y == x || y == w || z == x || z == w || z == y || (z && z == residual) || (residual == y && l.ld_residual != l.ld_y)) return DSV4V_ERR_INVALID_ARG;
   return guarded([&] { return forward(l, x, w, bias, residual, z, y, static_cast<cudaStream_t>(stream)); });
 }
 
@@ -450,8 +450,9 @@ dsv4v_status dsv4v_linear_backward(const dsv4v_linear* layer, const void* x, con
         (dw && (!x || !aligned_to(x, in))))
       return DSV4V_ERR_INVALID_ARG;
     if (dx && (dx == d_y || dx == w || dx == z || dx == x)) return DSV4V_ERR_INVALID_ARG;
-    if (dw && (dw == x || dw == w || dw == d_y || dw == z || dw == dx)) return DSV4V_ERR_INVALID_ARG;
+    if (dw && (dw == x || dw == d_y || dw == z || dw == dx)) return DSV4V_ERR_INVALID_ARG;
   }
+  if (dw && dw == w) return DSV4V_ERR_INVALID_ARG;  // without rows too, which clears dw
   int sms = 0;
   if (!query_device(&sms, nullptr)) return DSV4V_ERR_CUDA;
   const BackwardLayout bl = backward_layout(l, sms);
