@@ -572,12 +572,24 @@ dsv4v_status dsv4v_grad_norm(const dsv4v_grad* grads, int n_tensors, float* norm
  *            block of DSV4V_STATE_BLOCK elements (the last may be short): exp_avg = code * scale,
  *            exp_avg_sq = (code * scale)^2, the code being that of its root.  A scale is the
  *            smallest power of two (at least 2^-126) that brings its block to at most 448, 0 for a
- *            block of zeros; codes round to nearest even, a root above zero at least to the
+ *            block of zeros; codes round as state_rounding says, a root above zero at least to the
  *            smallest code, and what is not finite becomes the NaN code.  All zeros is the
  *            initial state.
+ *   state_rounding: of 8-bit states.
+ *     DSV4V_ROUND_STOCHASTIC is the one to train with.  A value goes to one of the two codes
+ *       around it, exp_avg so that its expectation is kept and exp_avg_sq so that the expectation
+ *       of (code * scale)^2 is: over many steps both follow the formula's averages.  The draws are
+ *       numbered by the step, the tensor's place in the list and the element (Philox 4x32-7), so
+ *       a repeated call repeats its results.
+ *     DSV4V_ROUND_NEAREST (0) is exact to half a step of the code, 3 to 6 % of the value, but only
+ *       for one step: a moment that moves by less than that in a step does not move at all.  With
+ *       beta2 above 0.87 exp_avg_sq stops growing after a few dozen steps and never decays (at
+ *       0.999 and gradients of 1 it stays at 1/64).  For moments that change by more, and for
+ *       converting states.
  *   weight_decay: of this tensor (norm scales and biases usually take 0).
  * No two tensors of a list may overlap. */
 #define DSV4V_STATE_BLOCK 256
+typedef enum { DSV4V_ROUND_NEAREST = 0, DSV4V_ROUND_STOCHASTIC = 1 } dsv4v_rounding;
 typedef struct {
   void* param;
   const void* grad;
@@ -590,6 +602,7 @@ typedef struct {
   dsv4v_dtype param_dtype;
   dsv4v_dtype grad_dtype;
   int state_bits;
+  int state_rounding;    /* dsv4v_rounding; 0 with 32-bit states */
   double weight_decay;
 } dsv4v_adamw_tensor;
 

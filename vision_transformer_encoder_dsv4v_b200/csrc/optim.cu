@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kThreads) k_grad_norm_final(const double* part
 constexpr int kStateBlock = 256;
 constexpr int kAdamChunk = kThreads * 8;
 
-enum : uint32_t { kParamBf16 = 1, kGradBf16 = 2, kState8 = 4, kMaster = 8, kVector = 16 };
+enum : uint32_t { kParamBf16 = 1, kGradBf16 = 2, kState8 = 4, kMaster = 8, kVector = 16, kStochastic = 32, kIndexShift = 8 };
 
 struct AdamEntry {
   void* param;
@@ -220,7 +220,7 @@ struct AdamEntry {
   int64_t n;
   double decay;
   uint32_t chunk0;
-  uint32_t flags;
+  uint32_t flags;  // the tensor's place in the call's list from bit kIndexShift on
 };
 struct AdamArgs {
   double lr, beta1, beta2;
@@ -257,8 +257,7 @@ __device__ __forceinline__ bool step_taken(const float* grad_norm) {
 
 // Biased exponent of the power-of-two scale of a block whose largest magnitude has the bits
 // `top`: the smallest 2^e with top / 2^e <= 448 = 1.75 * 2^8, e >= -126.  A power of two makes the
-// division exact, so only the rounding to e4m3 is lost, and costs no precision: e4m3 is a
-// floating type that needs the block's range, not its exact maximum.
+// division exact, so that a value changes by its rounding to e4m3 alone.
 __device__ __forceinline__ uint32_t scale_exponent(uint32_t top) {
   const int e = static_cast<int>(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
   return static_cast<uint32_t>(max(e, 1));
@@ -330,6 +329,46 @@ struct AdamScalars {
   float b1, c1, b2, c2, eps, clip, step_size, inv_root;
 };
 
+// Random words of a counter and a key: Philox 4x32 (Salmon, Moraes, Dror and Shaw, "Parallel random
+// numbers: as easy as 1, 2, 3", 2011) of seven rounds, the number their tests of randomness ask for.
+__device__ __forceinline__ void philox(uint4& c, uint32_t k0, uint32_t k1) {
+#pragma unroll
+  for (int r = 0; r < 7; ++r) {
+    const uint64_t a = static_cast<uint64_t>(0xD2511F53u) * c.x, b = static_cast<uint64_t>(0xCD9E8D57u) * c.z;
+    c = make_uint4(static_cast<uint32_t>(b >> 32) ^ c.y ^ k0, static_cast<uint32_t>(b),
+                   static_cast<uint32_t>(a >> 32) ^ c.w ^ k1, static_cast<uint32_t>(a));
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+}
+
+// Step of e4m3 at x >= 0 (2^-9 below 2^-6), and its inverse.
+__device__ __forceinline__ float code_step(float x, float& inverse) {
+  const uint32_t e = max(__float_as_uint(x) >> 23, 121u) - 3u;
+  inverse = __uint_as_float((254u - e) << 23);
+  return __uint_as_float(e << 23);
+}
+
+// One of the two e4m3 values around q, such that the expectation is q.
+__device__ __forceinline__ float round_value(float q, uint32_t word) {
+  float inv;
+  const float step = code_step(fabsf(q), inv), t = fabsf(q) * inv, k = floorf(t);
+  const float u = static_cast<float>(word >> 8) * 5.9604644775390625e-8f;  // 24 bits
+  return copysignf((u < t - k ? k + 1.0f : k) * step, q);
+}
+
+// One of the two e4m3 values around root = sqrt(x) (approximately), such that the expectation of its
+// square is x: it is the square that goes on as a moving average.
+__device__ __forceinline__ float round_root(float x, float root, uint32_t word) {
+  float inv;
+  const float step = code_step(root, inv), t = x * inv * inv;
+  float k = floorf(root * inv);
+  if (t < k * k) k -= 1.0f;  // the root's own error crossed a whole step
+  if (t >= (k + 1.0f) * (k + 1.0f)) k += 1.0f;
+  const float u = static_cast<float>(word >> 8) * 5.9604644775390625e-8f;
+  return (u * fmaf(2.0f, k, 1.0f) < fmaf(-k, k, t) ? k + 1.0f : k) * step;
+}
+
 // One AdamW step of the 8 elements that a thread holds:
 //   g' = g min(1, max_norm / norm);  m = b1 m + (1 - b1) g';  v = b2 v + (1 - b2) g'^2
 //   p = p - (lr decay p + (lr / (1 - b1^t)) m / (sqrt(v) / sqrt(1 - b2^t) + eps))
@@ -351,9 +390,15 @@ __device__ __forceinline__ void adam8(const AdamScalars& a, float decay, const f
   }
 }
 
-// Codes and scales of a block's new moments.
-__device__ __forceinline__ void adam_codes(const float (&m)[8], const float (&v)[8], const float (&root)[8], uint2& mc, uint2& vc,
-                                           float& m_scale, float& v_scale) {
+// Codes and scales of a block's new moments.  Rounded to nearest, a moment moves only by more than half a
+// step of its code, 3 to 6 %: an average that takes less than that of each gradient stands still.  Rounded
+// stochastically it moves as the formula does on average, by draws that the step, the tensor and the
+// element `i` number: a repeated call repeats its codes.  The draws and their comparisons are about 50
+// instructions an element (eight blocks 302 -> 457 us, bound by issue), so that they have a kernel of their
+// own (STOCHASTIC) and the others keep their registers.
+template <bool STOCHASTIC>
+__device__ __forceinline__ void adam_codes(const AdamEntry& e, int64_t step, int64_t i, const float (&m)[8], const float (&v)[8],
+                                           const float (&root)[8], uint2& mc, uint2& vc, float& m_scale, float& v_scale) {
   uint32_t m_top = warp_top(m, false), v_top = warp_top(v, false);
   const bool wild = max(m_top, v_top) >= 0x7f800000u;  // an infinity in the block, for the whole warp
   if (wild) {
@@ -370,10 +415,25 @@ __device__ __forceinline__ void adam_codes(const float (&m)[8], const float (&v)
   for (int j = 0; j < 8; ++j) {
     qm[j] = m[j] * m_inv;
     qr[j] = root[j] * r_inv;
+  }
+  if (STOCHASTIC && (e.flags & kStochastic)) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {  // the words of elements 2c and 2c + 1
+      const uint64_t group = static_cast<uint64_t>(i) / 8;
+      uint4 w = make_uint4(static_cast<uint32_t>(group), static_cast<uint32_t>(group >> 32) << 2 | c, static_cast<uint32_t>(step),
+                           static_cast<uint32_t>(step >> 32));
+      philox(w, e.flags >> kIndexShift, 0u);
+      qm[2 * c] = round_value(qm[2 * c], w.x);
+      qr[2 * c] = round_root(v[2 * c] * r_inv * r_inv, qr[2 * c], w.y);
+      qm[2 * c + 1] = round_value(qm[2 * c + 1], w.z);
+      qr[2 * c + 1] = round_root(v[2 * c + 1] * r_inv * r_inv, qr[2 * c + 1], w.w);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
     // A root above zero never becomes zero: m may still be large there, and m / eps would blow the
     // step up.
     if (v[j] > 0.0f && qr[j] < 0.001953125f) qr[j] = 0.001953125f;
-  }
   if (wild) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -387,8 +447,8 @@ __device__ __forceinline__ void adam_codes(const float (&m)[8], const float (&v)
 
 // The usual case, 8 elements that exist behind aligned pointers.  The types are template
 // parameters, so that all loads are issued before the first of them is waited for.
-template <uint32_t KIND>
-__device__ __forceinline__ void adam_whole(const AdamEntry& e, const AdamScalars& a, float decay, int64_t i, int lane) {
+template <uint32_t KIND, bool STOCHASTIC>
+__device__ __forceinline__ void adam_whole(const AdamEntry& e, const AdamScalars& a, float decay, int64_t step, int64_t i, int lane) {
   constexpr bool PB = KIND & kParamBf16, GB = KIND & kGradBf16, S8 = KIND & kState8, MASTER = KIND & kMaster;
   float g[8], p[8], m[8], v[8], root[8];
   uint2 mc, vc;
@@ -413,7 +473,7 @@ __device__ __forceinline__ void adam_whole(const AdamEntry& e, const AdamScalars
   store8(e.param, PB, true, i, 8, p);
   if constexpr (MASTER) store8(e.master, false, true, i, 8, p);
   if constexpr (S8) {
-    adam_codes(m, v, root, mc, vc, m_scale, v_scale);
+    adam_codes<STOCHASTIC>(e, step, i, m, v, root, mc, vc, m_scale, v_scale);
     store_codes(e.m, true, i, 8, mc);
     store_codes(e.v, true, i, 8, vc);
     if (lane == 0) {
@@ -428,7 +488,8 @@ __device__ __forceinline__ void adam_whole(const AdamEntry& e, const AdamScalars
 
 // A tensor's ragged end, and tensors that are not aligned: any types, `cnt` elements (at most 8; for
 // the lanes behind the end, 0 or less).
-__device__ __noinline__ void adam_ragged(const AdamEntry& e, const AdamScalars& a, float decay, int64_t i, int cnt, int lane) {
+template <bool STOCHASTIC>
+__device__ __noinline__ void adam_ragged(const AdamEntry& e, const AdamScalars& a, float decay, int64_t step, int64_t i, int cnt, int lane) {
   const bool vec = e.flags & kVector, s8 = e.flags & kState8, pb = e.flags & kParamBf16;
   const int64_t block = (i - lane * 8) / kStateBlock;
   float g[8], p[8], m[8], v[8], root[8];
@@ -450,7 +511,7 @@ __device__ __noinline__ void adam_ragged(const AdamEntry& e, const AdamScalars& 
   if (s8) {
     uint2 mc, vc;
     float m_scale, v_scale;
-    adam_codes(m, v, root, mc, vc, m_scale, v_scale);
+    adam_codes<STOCHASTIC>(e, step, i, m, v, root, mc, vc, m_scale, v_scale);
     __syncwarp();  // every lane has read the block's old scales
     store_codes(e.m, vec, i, cnt, mc);
     store_codes(e.v, vec, i, cnt, vc);
@@ -467,18 +528,21 @@ __device__ __noinline__ void adam_ragged(const AdamEntry& e, const AdamScalars& 
 // A CTA takes one chunk: CTAs that start in the chunks' order sweep each array front to back, which
 // HBM rewards (428 us for 103 M bf16 weights with fp32 masters and states, 3.08 GB; a persistent grid
 // that strides over the chunks took 536 us, contiguous ranges 527 us).
-template <int BYTES>
+template <int BYTES, bool STOCHASTIC>
 __global__ void __launch_bounds__(kThreads, 4) k_adamw(const __grid_constant__ AdamTable<BYTES> t) {
   grid_dependency_wait();
   if (!step_taken(t.a.grad_norm)) return;
   double lr = t.a.lr;
   float step_size = t.a.step_size, inv_root = t.a.inv_root;
+  int64_t step = STOCHASTIC ? t.a.step : 0;
   if (t.a.lr_dev || t.a.step_dev) {  // the schedule lies on the device
     __shared__ double s_lr;
     __shared__ float s_step_size, s_inv_root;
+    __shared__ int64_t s_step;
     if (threadIdx.x == 0) {
       if (t.a.lr_dev) lr = static_cast<double>(*t.a.lr_dev);
       const int64_t step = t.a.step_dev ? *t.a.step_dev + 1 : t.a.step;
+      if constexpr (STOCHASTIC) s_step = step;
       s_lr = lr;
       s_step_size = static_cast<float>(lr / (1.0 - int_power(t.a.beta1, step)));
       s_inv_root = static_cast<float>(1.0 / sqrt(1.0 - int_power(t.a.beta2, step)));
@@ -487,6 +551,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_adamw(const __grid_constant__ A
     lr = s_lr;
     step_size = s_step_size;
     inv_root = s_inv_root;
+    if constexpr (STOCHASTIC) step = s_step;
   }
   AdamScalars a{t.a.b1, t.a.c1, t.a.b2, t.a.c2, t.a.eps, 1.0f, step_size, inv_root};
   if (t.a.grad_norm && t.a.max_norm > 0.0f) a.clip = fminf(1.0f, __fdiv_rn(t.a.max_norm, *t.a.grad_norm));
@@ -499,21 +564,21 @@ __global__ void __launch_bounds__(kThreads, 4) k_adamw(const __grid_constant__ A
   const int64_t end = i - lane * 8 + 256;  // of the warp's elements
   if (end <= e.n && (e.flags & kVector)) {
     switch (e.flags & 15u) {
-      case 0: adam_whole<0>(e, a, decay, i, lane); break;
-      case kParamBf16: adam_whole<kParamBf16>(e, a, decay, i, lane); break;
-      case kGradBf16: adam_whole<kGradBf16>(e, a, decay, i, lane); break;
-      case kParamBf16 | kGradBf16: adam_whole<kParamBf16 | kGradBf16>(e, a, decay, i, lane); break;
-      case kState8: adam_whole<kState8>(e, a, decay, i, lane); break;
-      case kState8 | kParamBf16: adam_whole<kState8 | kParamBf16>(e, a, decay, i, lane); break;
-      case kState8 | kGradBf16: adam_whole<kState8 | kGradBf16>(e, a, decay, i, lane); break;
-      case kState8 | kParamBf16 | kGradBf16: adam_whole<kState8 | kParamBf16 | kGradBf16>(e, a, decay, i, lane); break;
-      case kMaster | kParamBf16: adam_whole<kMaster | kParamBf16>(e, a, decay, i, lane); break;
-      case kMaster | kParamBf16 | kGradBf16: adam_whole<kMaster | kParamBf16 | kGradBf16>(e, a, decay, i, lane); break;
-      case kMaster | kState8 | kParamBf16: adam_whole<kMaster | kState8 | kParamBf16>(e, a, decay, i, lane); break;
-      default: adam_whole<kMaster | kState8 | kParamBf16 | kGradBf16>(e, a, decay, i, lane); break;
+      case 0: adam_whole<0, STOCHASTIC>(e, a, decay, step, i, lane); break;
+      case kParamBf16: adam_whole<kParamBf16, STOCHASTIC>(e, a, decay, step, i, lane); break;
+      case kGradBf16: adam_whole<kGradBf16, STOCHASTIC>(e, a, decay, step, i, lane); break;
+      case kParamBf16 | kGradBf16: adam_whole<kParamBf16 | kGradBf16, STOCHASTIC>(e, a, decay, step, i, lane); break;
+      case kState8: adam_whole<kState8, STOCHASTIC>(e, a, decay, step, i, lane); break;
+      case kState8 | kParamBf16: adam_whole<kState8 | kParamBf16, STOCHASTIC>(e, a, decay, step, i, lane); break;
+      case kState8 | kGradBf16: adam_whole<kState8 | kGradBf16, STOCHASTIC>(e, a, decay, step, i, lane); break;
+      case kState8 | kParamBf16 | kGradBf16: adam_whole<kState8 | kParamBf16 | kGradBf16, STOCHASTIC>(e, a, decay, step, i, lane); break;
+      case kMaster | kParamBf16: adam_whole<kMaster | kParamBf16, STOCHASTIC>(e, a, decay, step, i, lane); break;
+      case kMaster | kParamBf16 | kGradBf16: adam_whole<kMaster | kParamBf16 | kGradBf16, STOCHASTIC>(e, a, decay, step, i, lane); break;
+      case kMaster | kState8 | kParamBf16: adam_whole<kMaster | kState8 | kParamBf16, STOCHASTIC>(e, a, decay, step, i, lane); break;
+      default: adam_whole<kMaster | kState8 | kParamBf16 | kGradBf16, STOCHASTIC>(e, a, decay, step, i, lane); break;
     }
   } else if (end - 256 < e.n) {
-    adam_ragged(e, a, decay, i, static_cast<int>(min(int64_t(8), e.n - i)), lane);
+    adam_ragged<STOCHASTIC>(e, a, decay, step, i, static_cast<int>(min(int64_t(8), e.n - i)), lane);
   }
 }
 
@@ -549,6 +614,8 @@ dsv4v_status check_grads(const dsv4v_grad* grads, int n_tensors) {
 dsv4v_status check_tensor(const dsv4v_adamw_tensor& t) {
   if (t.n < 0 || !known_dtype(t.param_dtype) || !known_dtype(t.grad_dtype) || (t.state_bits != 32 && t.state_bits != 8) ||
       !(t.weight_decay >= 0.0) || !std::isfinite(t.weight_decay))
+    return DSV4V_ERR_INVALID_ARG;
+  if (t.state_rounding != DSV4V_ROUND_NEAREST && (t.state_rounding != DSV4V_ROUND_STOCHASTIC || t.state_bits != 8))
     return DSV4V_ERR_INVALID_ARG;
   if (t.n == 0) return DSV4V_OK;
   if (!t.param || !t.grad || !t.exp_avg || !t.exp_avg_sq) return DSV4V_ERR_INVALID_ARG;
@@ -590,9 +657,11 @@ int launch_adamw(const AdamArgs& args, const dsv4v_adamw_tensor* tensors, int i,
   t.a = args;
   t.chunks = 0;
   t.count = 0;
+  bool stochastic = false;
   for (; i < n && t.count < t.CAP; ++i) {
     const dsv4v_adamw_tensor& x = tensors[i];
     if (x.n == 0) continue;
+    stochastic |= x.state_rounding == DSV4V_ROUND_STOCHASTIC;
     const bool s8 = x.state_bits == 8;
     const size_t state_align = s8 ? 8 : 16;
     const bool vec = aligned_to(x.param, 16) && aligned_to(x.grad, 16) && (!x.master || aligned_to(x.master, 16)) &&
@@ -600,11 +669,14 @@ int launch_adamw(const AdamArgs& args, const dsv4v_adamw_tensor* tensors, int i,
     t.e[t.count++] = AdamEntry{x.param, x.grad, x.master, x.exp_avg, x.exp_avg_sq, x.exp_avg_scale, x.exp_avg_sq_scale, x.n,
                                x.weight_decay, t.chunks,
                                (x.param_dtype == DSV4V_BF16 ? kParamBf16 : 0u) | (x.grad_dtype == DSV4V_BF16 ? kGradBf16 : 0u) |
-                                   (s8 ? kState8 : 0u) | (x.master ? kMaster : 0u) | (vec ? kVector : 0u)};
+                                   (s8 ? kState8 : 0u) | (x.master ? kMaster : 0u) | (vec ? kVector : 0u) |
+                                   (x.state_rounding == DSV4V_ROUND_STOCHASTIC ? kStochastic : 0u) |
+                                   static_cast<uint32_t>(i) << kIndexShift};
     t.chunks += chunks_of(x.n, kAdamChunk);
   }
   if (t.count == 0) return i;
-  return launch_pdl(k_adamw<BYTES>, dim3(t.chunks), dim3(kThreads), 0, s, t) == cudaSuccess ? i : -1;
+  const auto kernel = stochastic ? k_adamw<BYTES, true> : k_adamw<BYTES, false>;
+  return launch_pdl(kernel, dim3(t.chunks), dim3(kThreads), 0, s, t) == cudaSuccess ? i : -1;
 }
 
 }  // namespace

@@ -47,6 +47,7 @@ EXPORTS = ("dsv4v_workspace_size", "dsv4v_rope2d_table", "dsv4v_block_forward", 
 DSV4V_NOALLOC_MAX_ROWS = 65536
 ACT_NONE, ACT_GELU, ACT_SILU = 0, 1, 2  # DSV4V_ACT_*
 DSV4V_STATE_BLOCK = 256  # elements that share one scale of an 8-bit optimizer state
+ROUND_NEAREST, ROUND_STOCHASTIC = 0, 1  # DSV4V_ROUND_*
 
 
 class Dsv4vError(RuntimeError):
@@ -92,7 +93,8 @@ class AdamwTensor(ctypes.Structure):
     _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("master", ctypes.c_void_p),
                 ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p), ("exp_avg_scale", ctypes.c_void_p),
                 ("exp_avg_sq_scale", ctypes.c_void_p), ("n", ctypes.c_int64), ("param_dtype", ctypes.c_int),
-                ("grad_dtype", ctypes.c_int), ("state_bits", ctypes.c_int), ("weight_decay", ctypes.c_double)]
+                ("grad_dtype", ctypes.c_int), ("state_bits", ctypes.c_int), ("state_rounding", ctypes.c_int),
+                ("weight_decay", ctypes.c_double)]
 
 
 class AdamwConfig(ctypes.Structure):
@@ -613,7 +615,8 @@ class AdamwTable:
     tensors param, grad, exp_avg, exp_avg_sq, optionally master (fp32, of a bf16 param) and
     weight_decay (a number, 0 by default); for 8-bit states (uint8 or float8_e4m3fn exp_avg and
     exp_avg_sq) exp_avg_scale and exp_avg_sq_scale too, fp32, one value per DSV4V_STATE_BLOCK
-    elements."""
+    elements, and state_rounding: ROUND_STOCHASTIC, to train with, or ROUND_NEAREST (the default), whose
+    moments stand still where a step moves them by less than half a code (see dsv4v_adamw_tensor)."""
 
     def __init__(self, tensors):
         import torch
@@ -651,7 +654,7 @@ class AdamwTable:
             self.c[i] = AdamwTensor(address(i, t, "param", any_float, n), address(i, t, "grad", any_float, n), master,
                                     address(i, t, "exp_avg", state, n), address(i, t, "exp_avg_sq", state, n), m_scale,
                                     v_scale, n, _dtype_code(p, "param"), _dtype_code(t["grad"], "grad"), 8 if eight else 32,
-                                    float(t.get("weight_decay") or 0.0))
+                                    t.get("state_rounding") or ROUND_NEAREST, float(t.get("weight_decay") or 0.0))
         written.sort()
         for (_, end, i), (begin, _, j) in zip(written, written[1:]):
             if begin < end:
