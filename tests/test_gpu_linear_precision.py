@@ -1,0 +1,83 @@
+"""The fp32 Linear layer keeps fp32's precision over fp32's range: the bounds of linear_precision.py."""
+import linear_precision as P
+import numpy as np
+import pytest
+import torch
+
+from vision_transformer_encoder_dsv4v_b200 import dsv4v as A
+
+pytestmark = pytest.mark.gpu
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def normal(shape, seed):
+    return torch.randn(shape, generator=torch.Generator().manual_seed(seed)).cuda()
+
+
+def forward(x, w):
+    (rows, k), n = x.shape, w.shape[0]
+    y = torch.empty(rows, n, device="cuda")
+    A.dsv4v_linear_forward(A.make_linear(rows, k, n, dtype=A.DSV4V_F32), x, w, None, None, None, y)
+    assert A.dsv4v_device_error() == 0
+    return np64(y), np64(x) @ np64(w).T
+
+
+def backward(x, w, d_y):
+    (rows, k), n = x.shape, w.shape[0]
+    layer = A.make_linear(rows, k, n, dtype=A.DSV4V_F32)
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    ws = torch.empty(A.dsv4v_linear_backward_workspace_size(layer), dtype=torch.uint8, device="cuda")
+    A.dsv4v_linear_backward(layer, x, w, None, d_y, dx, dw, None, ws)
+    assert A.dsv4v_device_error() == 0
+    return (np64(dx), np64(d_y) @ np64(w)), (np64(dw), np64(d_y).T @ np64(x))
+
+
+# One row of an operand at each scale, against an operand of about 2^`other`: each row's own error, from values whose low
+# parts bf16 cannot hold (below 2^-110) and subnormal ones to values whose bf16 parts overflow.
+SCALES = [0, -60, -95, -108, -115, -125, -133, -140, 30, 60, 100, 113, 126]
+
+
+def scaled(k, seed):
+    rows = torch.tensor([2.0 ** s for s in SCALES], dtype=torch.float64)[:, None]
+    return (normal((len(SCALES), k), seed).cpu().double().clamp(-1.9, 1.9) * rows).float().cuda()
+
+
+@pytest.mark.parametrize("k,n", [(100, 70), (588, 201), (4600, 40)])
+@pytest.mark.parametrize("other", [-8, 20])
+def test_forward_rows_of_every_scale(k, n, other):
+    # the results stay between 2^-125 and the end of fp32's range for the rows that are looked at
+    x = scaled(k, 1)
+    use = [i for i, s in enumerate(SCALES) if -120 <= s + other <= 115]
+    keep = torch.zeros(len(SCALES), 1, device="cuda")
+    keep[use] = 1
+    y, want = forward(x * keep, normal((n, k), 2) * 2.0 ** other)
+    for i in use:
+        assert P.relative(y[i], want[i]) <= P.FROBENIUS, (SCALES[i], P.relative(y[i], want[i]))
+
+
+@pytest.mark.parametrize("k,n", [(100, 70), (588, 201)])
+def test_tiny_operands_meet_large_ones(k, n):
+    # 2^-140 to 2^-95 against 2^100
+    low = [i for i, s in enumerate(SCALES) if s <= -95]
+    x = scaled(k, 1)[low].contiguous()
+    w = normal((n, k), 2) * 2.0 ** 100
+    y, want = forward(x, w)
+    for i in range(len(low)):
+        assert P.relative(y[i], want[i]) <= P.FROBENIUS, (SCALES[low[i]], P.relative(y[i], want[i]))
+
+
+@pytest.mark.parametrize("rows,k,n", [(50, 100, 13), (300, 130, 13)])
+def test_gradients_of_tiny_operands(rows, k, n):
+    # d_y's columns at 2^-140 to 1 (dw's rows), then its rows (dx's)
+    cols = torch.tensor([2.0 ** s for s in np.linspace(-140, 0, n)], dtype=torch.float64)
+    x, w = normal((rows, k), 1) * 2.0 ** 60, normal((n, k), 2) * 2.0 ** 60
+    d_y = (normal((rows, n), 3).cpu().double() * cols).float().cuda()
+    _, (dw, want) = backward(x, w, d_y)
+    assert max(P.relative(dw[i], want[i]) for i in range(n)) <= P.FROBENIUS
+    down = torch.tensor([2.0 ** s for s in np.linspace(-140, 0, rows)], dtype=torch.float64)
+    d_y = (normal((rows, n), 3).cpu().double() * down[:, None]).float().cuda()
+    (dx, want), _ = backward(x, w, d_y)
+    assert max(P.relative(dx[i], want[i]) for i in range(rows)) <= P.FROBENIUS

@@ -1,8 +1,9 @@
 // The Linear layer's fp32 products on the bf16 tensor cores.
 //
 // A value is the sum of three bf16, x = x0 + x1 + x2 with |x1| <= 2^-8 |x| and |x2| <= 2^-16 |x| (8 bits
-// of its mantissa each), exactly so above 2^-110.  Of the nine products of two values the six largest
-// are formed,
+// of its mantissa each).  Both operands are split as 2^16 x, whose last bit is at least bf16's least value
+// (2^-133): the three parts are then exact down to fp32's own least value, and the sums are scaled back.
+// Of the nine products of two values the six largest are formed,
 //   a b = a0 b0 + (a0 b1 + a1 b0) + (a0 b2 + a1 b1 + a2 b0) + O(2^-25 |a b|),
 // in three MMAs, because the parts of B lie behind one another as more columns: a0 meets b0, b1 and
 // b2, a1 meets b0 and b1, a2 meets b0.  The tensor core truncates as it accumulates (2^-23 of the sum
@@ -41,16 +42,20 @@ constexpr int kSumLd = TN + 1;
 constexpr int kSumRows = TM + 32;  // with the rows that an unrolled read may touch behind the tile
 static_assert(kSumRows * kSumLd * 4 <= kStages * kStageBytes, "the sums have to fit the ring");
 
-// bf16 parts of eight values, 16 bytes each.  A value that is not finite, or that rounds to a bf16
-// infinity, gives parts that are not finite, and so are the sums that it enters: their tiles are
-// computed again in fp32 (see store_column_plain).
+constexpr float kScale = 65536.0f, kUnscale = 1.0f / (kScale * kScale);
+
+// bf16 parts of eight values times kScale, 16 bytes each.  A value that is not finite, or (from 2^111 on)
+// whose multiple rounds to a bf16 infinity, gives parts that are not finite, and so are the sums that it
+// enters: their tiles are computed again in fp32 (see store_column_plain).
 __device__ __forceinline__ void split8(const float (&x)[8], uint4 (&out)[3]) {
   uint32_t w[3][4];
 #pragma unroll
   for (int h = 0; h < 4; ++h) {
     float a, b;
-    w[0][h] = pack_bf16x2(x[2 * h], x[2 * h + 1]);
-    const uint64_t r = sub2(pk2(x[2 * h], x[2 * h + 1]), bf16x2_f2(w[0][h]));
+    const uint64_t scaled = mul2(pk2(x[2 * h], x[2 * h + 1]), pk2(kScale, kScale));
+    upk2(scaled, a, b);
+    w[0][h] = pack_bf16x2(a, b);
+    const uint64_t r = sub2(scaled, bf16x2_f2(w[0][h]));
     upk2(r, a, b);
     w[1][h] = pack_bf16x2(a, b);
     upk2(sub2(r, bf16x2_f2(w[1][h])), a, b);
@@ -327,8 +332,8 @@ __device__ __forceinline__ void compute_tile(const ProductF32& job, int64_t m_ti
       bool fine = true;
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        sums[(quad * 32 + lane) * kSumLd + col + j] = v[j];
-        fine = fine && fabsf(v[j]) <= 1e37f;  // eight of these stay below the end of fp32's range
+        sums[(quad * 32 + lane) * kSumLd + col + j] = v[j] * kUnscale;
+        fine = fine && fabsf(v[j]) <= 1e37f;  // far below the end of the accumulators' range
       }
       if (!fine && m0 + quad * 32 + lane < M) *wild = 1;
     }
