@@ -32,6 +32,15 @@ def products(a, b, pairs=PAIRS):
 FROBENIUS = 13 * U
 
 
+# Each element, S being the sum of its terms' magnitudes: 16 additions on the tensor core drop at most 2 u of the sum so
+# far, and the alignment of each one's sixteen terms 2 u of those: 34 u S (and 2^-8 of that in the smaller products'
+# columns).  The products left out are 2 u S.  The fp32 additions of K / 256 sums, of eight ranks and of three columns
+# round by one u each.
+def element_tolerance(a, b):
+    a, b = np.abs(np.asarray(a, dtype=np.float64)), np.abs(np.asarray(b, dtype=np.float64))
+    return (34 + 1 + 2 + a.shape[1] / 256 + 11) * U * (a @ b.T)
+
+
 def relative(got, want):
     return np.linalg.norm(np.asarray(got, dtype=np.float64) - want) / np.linalg.norm(want)
 

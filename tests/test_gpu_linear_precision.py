@@ -81,3 +81,40 @@ def test_gradients_of_tiny_operands(rows, k, n):
     d_y = (normal((rows, n), 3).cpu().double() * down[:, None]).float().cuda()
     (dx, want), _ = backward(x, w, d_y)
     assert max(P.relative(dx[i], want[i]) for i in range(rows)) <= P.FROBENIUS
+
+
+# ---------------------------------------------------------------------------------------------- all six products
+@pytest.mark.parametrize("rows,k,n", [(5, 257, 1000), (63, 17, 65), (130, 588, 97), (777, 588, 201), (300, 300, 130), (129, 256, 64),
+                                      (70, 1100, 60), (777, 588, 1001), (40, 4000, 72), (2, 4608, 40)])
+def test_forward_is_as_near_as_all_products_make_it(rows, k, n):
+    x, w = normal((rows, k), 1), normal((n, k), 2)
+    y, want = forward(x, w)
+    assert P.relative(y, want) <= P.FROBENIUS
+    assert np.all(np.abs(y - want) <= P.element_tolerance(np64(x), np64(w)))
+
+
+@pytest.mark.parametrize("rows,k,n", [(63, 17, 65), (130, 588, 97), (777, 588, 201), (257, 64, 1000), (300, 130, 300), (777, 588, 1001),
+                                      (2100, 400, 1001), (4000, 64, 72)])
+def test_gradients_are_as_near_as_all_products_make_them(rows, k, n):
+    x, w, d_y = normal((rows, k), 1), normal((n, k), 2), normal((rows, n), 3)
+    operands = ((np64(d_y), np64(w).T), (np64(d_y).T, np64(x).T))
+    for (got, want), (a, b) in zip(backward(x, w, d_y), operands):
+        assert P.relative(got, want) <= P.FROBENIUS
+        assert np.all(np.abs(got - want) <= P.element_tolerance(a, b))
+
+
+@pytest.mark.parametrize("kind", P.KINDS)
+@pytest.mark.parametrize("groups", [9, 150, 1000])
+@pytest.mark.parametrize("where", ["forward", "dx", "dw"])
+def test_sums_that_are_left_of_low_parts(kind, groups, where):
+    # rows 90, columns 70, a contraction of 4 groups: the forward's over features, dx's over outputs, dw's over rows
+    a, b = P.cancelling(kind, groups, 90, 70)
+    want = a.astype(np.float64) @ b.astype(np.float64).T
+    dev = lambda x: torch.from_numpy(np.ascontiguousarray(x)).cuda()  # noqa: E731
+    if where == "forward":
+        got = forward(dev(a), dev(b))[0]
+    elif where == "dx":  # d_y . w
+        got = backward(normal((90, 70), 1), dev(b.T), dev(a))[0][0]
+    else:  # d_y^T . x
+        got = backward(dev(b.T), normal((90, 70), 1), dev(a.T))[1][0]
+    assert np.all(np.abs(got - want) <= P.cancelling_tolerance(a, b))
