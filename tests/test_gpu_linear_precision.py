@@ -118,3 +118,49 @@ def test_sums_that_are_left_of_low_parts(kind, groups, where):
     else:  # d_y^T . x
         got = backward(dev(b.T), normal((90, 70), 1), dev(a.T))[1][0]
     assert np.all(np.abs(got - want) <= P.cancelling_tolerance(a, b))
+
+
+# ---------------------------------------------------------------------------------------------- what is not finite
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), 3e38, 1e34])
+@pytest.mark.parametrize("rows,k,n", [(40, 100, 70), (300, 300, 130), (777, 588, 201), (60, 2100, 40)])
+def test_a_value_that_bf16_cannot_hold_changes_its_own_sums_alone(rows, k, n, bad):
+    # the other sums of its tiles keep their bits
+    x, w, d_y = normal((rows, k), 1), normal((n, k), 2), normal((rows, n), 3)
+    b, r = normal((n,), 4), normal((rows, n), 5)
+    layer = A.make_linear(rows, k, n, A.ACT_GELU, A.DSV4V_F32)
+
+    def forward_all(x):
+        y, z = torch.empty(rows, n, device="cuda"), torch.empty(rows, n, device="cuda")
+        A.dsv4v_linear_forward(layer, x, w, b, r, z, y)
+        return y, z
+
+    def backward_all(x, d_y):
+        plain = A.make_linear(rows, k, n, dtype=A.DSV4V_F32)
+        dx, dw = torch.empty_like(x), torch.empty_like(w)
+        ws = torch.empty(A.dsv4v_linear_backward_workspace_size(plain), dtype=torch.uint8, device="cuda")
+        A.dsv4v_linear_backward(plain, x, w, None, d_y, dx, dw, None, ws)
+        return dx, dw
+
+    i, c, f = rows // 2, k // 3, n // 2
+    clean_y, clean_z = forward_all(x)
+    clean_dx, clean_dw = backward_all(x, d_y)
+    x1, d1 = x.clone(), d_y.clone()
+    x1[i, c], d1[i, f] = bad, bad
+    others = torch.arange(rows, device="cuda") != i
+    for got, want in zip(forward_all(x1), (clean_y, clean_z)):
+        assert torch.equal(got[others], want[others])
+    z = forward_all(x1)[1][i].double().cpu().numpy()
+    with np.errstate(invalid="ignore", over="ignore"):
+        want = np64(x1[i]) @ np64(w).T + np64(b)
+    fits = np.abs(want) <= np.finfo(np.float32).max
+    assert np.array_equal(np.isnan(z), np.isnan(want))
+    assert np.all(np.abs(z[fits] - want[fits]) <= 2.0 ** -20 * np.abs(want[fits]))
+    # a gradient of one output: its row of dx and its row of dw; a value of x: its column of dw
+    dx, _ = backward_all(x, d1)
+    assert torch.equal(dx[others], clean_dx[others])
+    _, dw = backward_all(x, d1)
+    rest = torch.arange(n, device="cuda") != f
+    assert torch.equal(dw[rest], clean_dw[rest])
+    _, dw = backward_all(x1, d_y)
+    rest = torch.arange(k, device="cuda") != c
+    assert torch.equal(dw[:, rest], clean_dw[:, rest])
