@@ -310,12 +310,11 @@ dsv4v_status forward(const Layer& l, const void* x, const void* w, const float* 
   e.z = static_cast<__nv_bfloat16*>(z);
   e.ld_z = l.ld_z;
   e.act = l.act;
-  if (linear_is_few(l.rows, l.k)) {
-    int sms = 0;
-    if (!query_device(&sms, nullptr)) return DSV4V_ERR_CUDA;
+  int sms = 0;
+  if (!query_device(&sms, nullptr)) return DSV4V_ERR_CUDA;
+  if (linear_is_few(l.rows, l.n, l.k, sms))
     return cuda_status(launch_linear_few(x, l.ld_x, w, l.ld_w, static_cast<int>(l.rows), static_cast<int>(l.n), static_cast<int>(l.k), e,
                                          sms, s));
-  }
   e.vec_io = rows16(y, l.ld_y) && rows16(residual, l.ld_residual) && rows16(z, l.ld_z);
   return gemm(LINEAR_FORWARD, Operand{x, l.ld_x}, Operand{w, l.ld_w}, l.rows, l.n, l.k, e, s);
 }

@@ -67,7 +67,7 @@ inline int linear_box_a(const LinearPlan& p, bool a_mn) { return a_mn ? linear_d
 inline int linear_box_b(const LinearPlan& p, bool b_mn) { return b_mn ? linear_depth(p) : (p.pair ? p.bn / 2 : p.bn); }
 
 // The forward of a few rows without tensor cores, and whether it is taken.
-bool linear_is_few(int64_t M, int64_t K);
+bool linear_is_few(int64_t M, int64_t N, int64_t K, int sms);
 cudaError_t launch_linear_few(const void* x, int64_t ld_x, const void* w, int64_t ld_w, int M, int N, int K, const LinearEpilogue& e,
                               int sms, cudaStream_t s);
 

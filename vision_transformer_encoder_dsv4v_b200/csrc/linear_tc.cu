@@ -939,8 +939,14 @@ cudaError_t launch_few(const void* x, int64_t ld_x, const void* w, int64_t ld_w,
 
 // Up to four rows, as long as they fit shared memory and the sharing of x does not cost more than
 // the tensor-core kernel's set-up (1 x 4608 x 4608: 9.5 us against 12.0 us; 2 rows 10.6 against 12.2;
-// 4 rows of 1024 x 2816 4.1 against 5.0, of 2816 x 1024 5.9 against 5.3).
-bool linear_is_few(int64_t M, int64_t K) { return M <= 2 ? M * K * 4 <= kFewSmem : (M <= 4 && K <= 2048); }
+// 4 rows of 1024 x 2816 4.1 against 5.0, of 2816 x 1024 5.9 against 5.3).  From two rows on, while the
+// features take one round of the CTAs, 16 each, that the SMs hold at two: 2048 -> 4096 with 4 rows 6.8 against
+// 7.6 us, 2048 -> 5632 10.2 against 8.1, 1824 -> 7656 17.0 against 8.9.  One row stays within 17 % of the other
+// kernel wherever it is slower (1528 -> 12000: 11.4 against 9.9).
+bool linear_is_few(int64_t M, int64_t N, int64_t K, int sms) {
+  if (M == 1) return K * 4 <= kFewSmem;
+  return N <= 32 * sms && (M == 2 ? M * K * 4 <= kFewSmem : (M <= 4 && K <= 2048));
+}
 
 cudaError_t launch_linear_few(const void* x, int64_t ld_x, const void* w, int64_t ld_w, int M, int N, int K, const LinearEpilogue& e,
                               int sms, cudaStream_t s) {
