@@ -78,7 +78,10 @@ __device__ __forceinline__ void put8(float* p, const float (&v)[8]) {
 constexpr int kDzCols = 256;  // columns of a CTA: 32 threads of 8, by 8 rows at a time
 
 // One pass over dy (and z): writes dz where it is wanted and, per strip of rows, the column sums of
-// the unrounded dz, whose strips k_column_sums adds in order.  HBM bounds it (8192 x 4096 bf16, dy and z
+// the unrounded dz, whose strips k_column_sums adds in order.  In bf16, dz is rounded because it is an operand
+// of tcgen05 products beside the bf16 w and x: dx and dw are then two roundings from exact (2.35e-3 of their
+// norm) instead of one (1.66e-3).  As two bf16 parts it would cost both products twice (of the 495 us of 8192 x
+// 4608 -> 4096 they are about 460).  HBM bounds it (8192 x 4096 bf16, dy and z
 // read: 25 us, 5.3 TB/s, with four CTAs an SM of two rows in flight a thread; 34 us with two CTAs of
 // four).  VEC: rows are 16-byte aligned.
 template <class T, int ACT, bool VEC>

@@ -10,7 +10,8 @@
 // an addition): the large products have columns of their own, and every 256 of the contraction all of
 // them are added up in fp32 registers.  The result is about as far from the exact one as an fp32 dot
 // product (2e-7), at 3 bf16 MMAs of 64, 128 and 192 columns in the place of 64 columns of FMAs: 777 x
-// 1001 x 588 takes 13 us, where 4 x 4-output FMA tiles took 46 us, bound by shared-memory reads.
+// 588 -> 1001 takes 20 us (ten stages are 12 of them), 22.5 us with bias, GELU and residual, where 4 x 4-output
+// FMA tiles took 46 us, bound by shared-memory reads.
 //
 // Roles (544 threads): warps 0 to 15 load fp32, split it and write the parts into a 3-stage ring
 // (K-major, 128-byte swizzle, transposing where the contraction is not contiguous), and add up the
@@ -477,8 +478,9 @@ cudaError_t launch_product(const ProductF32& p, const ColumnSums& cs, uint32_t* 
 
 // ---------------------------------------------------------------------------- a few rows
 // y of one to four rows: a warp streams the weights of an output feature at a time against the rows
-// of x in shared memory, as k_linear_few does for bf16 (1 x 1024 x 1024: 3 us, where a 128-row tile
-// takes 12 us).
+// of x in shared memory, as k_linear_few does for bf16 (1 x 1024 x 1024: 3.1 us, where a 128-row tile
+// takes 12 us; 1 x 4608 x 4608: 23.8 us, 12.9 of them its 85 MB at the copy rate: the stream starts only once
+// x is staged).
 constexpr int kFewThreads = 256, kFewSmem = 48 * 1024;
 
 template <int R>
