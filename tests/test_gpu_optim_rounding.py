@@ -212,3 +212,44 @@ def test_stochastic_moments_follow_the_averages(kind):
             want = lr * (M / (1 - 0.9 ** step)).abs() / (V / (1 - 0.999 ** step)).sqrt()
             ratio = float(t["param"].double().abs().mean() / want.mean())
             assert 0.95 <= ratio <= 1.25, (step, ratio)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("decay", [0.0, 0.1])
+@pytest.mark.parametrize("n", [13, 600])
+def test_adamw_leaves_infinite_weights_infinite(bits, decay, n):
+    # p (1 - lr decay) - update, as for a bias that masks with its infinities
+    p = torch.randn(n, generator=torch.Generator().manual_seed(1)).cuda()
+    p[3], p[9], p[11] = float("-inf"), float("inf"), float("nan")
+    was = p.clone()
+    t = {"param": p, "grad": torch.ones(n, device="cuda"), "weight_decay": decay}
+    dtype = torch.uint8 if bits == 8 else torch.float32
+    t["exp_avg"], t["exp_avg_sq"] = torch.zeros(n, dtype=dtype, device="cuda"), torch.zeros(n, dtype=dtype, device="cuda")
+    if bits == 8:
+        t["exp_avg_scale"], t["exp_avg_sq_scale"] = (torch.zeros((n + 255) // 256, device="cuda") for _ in range(2))
+    A.dsv4v_adamw_step(A.make_adamw(1e-2), A.AdamwTable([t]))
+    assert p[3] == float("-inf") and p[9] == float("inf") and torch.isnan(p[11])
+    rest = torch.isfinite(was)
+    want = was[rest] * (1 - 1e-2 * decay) - 1e-2
+    assert torch.allclose(p[rest], want, rtol=1e-5, atol=1e-6)
+
+
+@pytest.mark.parametrize("count", [3, 500])
+def test_roundings_side_by_side(count):
+    # tensors of both roundings in one call, more than a launch takes too: each has the codes that its own rounding
+    # gives it, and a tensor rounded to nearest those of a call without the others
+    make = lambda: [dict(make8(40 + i % 300, i), state_rounding=i % 2) for i in range(count)]  # noqa: E731
+    both, nearest = make(), [t for t in make() if not t["state_rounding"]]
+    before = [(np64(t["param"]), np64(t["grad"]), *moments(t)) for t in both]
+    A.dsv4v_adamw_step(A.make_adamw(step=9, **HYPER), A.AdamwTable(both))
+    A.dsv4v_adamw_step(A.make_adamw(step=9, **HYPER), A.AdamwTable(nearest))
+    for a, b in zip([t for t in both if not t["state_rounding"]], nearest):
+        assert all(torch.equal(a[k], b[k]) for k in ("param", "exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale"))
+    off = total = 0
+    for i, (t, (p, g, m, v)) in enumerate(zip(both, before)):
+        if t["state_rounding"]:
+            qm, qr, _, _ = O.stochastic_codes(*O.adamw(p, g, m, v, 9, decay=0.1, **HYPER)[1:], 9, i)
+            for key, want in (("exp_avg", qm), ("exp_avg_sq", qr)):
+                off += int((O.e4m3_values()[t[key].cpu().numpy()] != want).sum())
+                total += len(want)
+    assert off <= 1 + 1e-4 * total

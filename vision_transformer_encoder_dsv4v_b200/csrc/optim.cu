@@ -386,7 +386,8 @@ __device__ __forceinline__ void adam8(const AdamScalars& a, float decay, const f
     m[j] = __fadd_rn(__fmul_rn(m[j], a.b1), __fmul_rn(gj, a.c1));
     v[j] = __fadd_rn(__fmul_rn(v[j], a.b2), __fmul_rn(__fmul_rn(gj, gj), a.c2));
     root[j] = sqrt_approx(v[j]);
-    p[j] -= fmaf(decay, p[j], a.step_size * m[j] * rcp_approx(fmaf(root[j], a.inv_root, a.eps)));
+    const float update = a.step_size * m[j] * rcp_approx(fmaf(root[j], a.inv_root, a.eps));
+    p[j] -= fabsf(p[j]) <= 3.4028235e38f ? fmaf(decay, p[j], update) : update;  // a weight that masks by its infinity keeps it
   }
 }
 
