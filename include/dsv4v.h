@@ -517,6 +517,8 @@ typedef struct {
  *   z: device [rows, out_features], written for dsv4v_linear_backward, or NULL.
  *   y: device [rows, out_features], written.  Elements between a row's end and the next row are
  *   left as they were.
+ * In DSV4V_F32 a sum that is beyond 2^91 or meets an operand from 2^111 on, an infinity or NaN is
+ * formed by itself: as exact as the others, but slow where many are.
  * Needs no workspace; the result does not depend on the schedule.  Unlike the calls above, this one
  * and dsv4v_linear_backward read nothing, w included, before the kernels ahead of them on the stream
  * have finished: w may be another call's output. */

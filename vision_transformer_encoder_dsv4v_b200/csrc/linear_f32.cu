@@ -179,7 +179,7 @@ __device__ __forceinline__ void store_column(const EpilogueF32& e, int lr, int r
 // ranks: such a sum is formed again from plain fp32 products of the operands, where an infinity meets no
 // zeros among the other operand's parts and a large value is not rounded to one; the other sums stay as
 // they are.  A sum that has become NaN is not looked at further.  16384 x 1024 -> 1024 takes 396 us, with one
-// NaN 400 us, of NaN alone 8.3 ms.
+// NaN 400 us, of NaN alone 8.3 ms, with every sum beyond 2^91 78 ms.
 template <bool A_K, bool B_K>
 __device__ __noinline__ void store_column_plain(const EpilogueF32& e, const float* a, int64_t lda, const float* b, int64_t ldb, int64_t K,
                                                 int64_t row, int64_t row_end, int64_t col, const float* sum, int ks) {
